@@ -10,6 +10,9 @@ PyTorch fallback: if the library is missing, every call raises.
     copy_blocks(k_cache, v_cache, src, dst)      # copy-on-write, on the device
     BlockManager(num_blocks)                     # host: tables, counts, forks
 
+``operators.py`` adds the rotation of positions on the way into the cache, block-scaled
+E4M3 pools and attention with capped, biased or windowed scores.
+
 Tensors are torch CUDA tensors on the current device: bf16 K/V/Q laid out as
 ``include/pkv.h`` describes (pools ``[num_blocks, 16, num_kv_heads, head_dim]``),
 int64 slot mapping, int32 block tables and context lengths. Calls are enqueued
@@ -37,6 +40,7 @@ BLOCK_SIZE = 16
 # function name -> (argtypes, restype); mirrors include/pkv.h
 _P, _I32, _I64, _SZ, _F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                           ctypes.c_float)
+_D = ctypes.c_double
 SIGNATURES = {
     "pkv_kv_append": ([_P, _P, _P, _I64, _P, _P, _I64, _I32, _I32, _P], ctypes.c_int),
     "pkv_workspace_size": ([_I32, _I32, _I32, _I32, _I32], _SZ),
@@ -71,6 +75,20 @@ SIGNATURES = {
     "pkv_kv_append_fp8": ([_P, _P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
     "pkv_paged_decode_attention_fp8": ([_P, _P, _P, _I64, _P, _P, _P, _I32, _P, _I32, _I32, _I32,
                                         _I32, _I32, _F, _P, _I32, _P, _SZ, _P], ctypes.c_int),
+    # operators beside the decode path (include/pkv_ops.h)
+    "pkv_rotary_turns": ([_I32, _D, _I32, _D, _D, _D, _D, _P], ctypes.c_int),
+    "pkv_rope_kv_append": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _I64,
+                            _I32, _I32, _I32, _I32, _I32, _F, _P], ctypes.c_int),
+    "pkv_rope_kv_append_fp8_block": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _P,
+                                      _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _F, _P],
+                                     ctypes.c_int),
+    "pkv_workspace_size_scored": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "pkv_paged_decode_attention_scored": ([_P, _P, _P, _I64, _P, _P, _P, _I32, _P, _I32, _I32,
+                                           _I32, _I32, _I32, _F, _F, _P, _I32, _P, _I32, _P, _SZ,
+                                           _P], ctypes.c_int),
+    "pkv_paged_decode_attention_fp8_block": ([_P, _P, _P, _I64, _P, _P, _P, _I32, _P, _I32, _I32,
+                                              _I32, _I32, _I32, _F, _P, _I32, _P, _SZ, _P],
+                                             ctypes.c_int),
     # host block manager (include/pkv_block_manager.h)
     "pkv_bm_create": ([_I64], _P),
     "pkv_bm_destroy": ([_P], None),
@@ -745,3 +763,8 @@ def decode_step_host(host_arena, device_arena, k_cache, v_cache, num_seqs, n_que
     if st != PKV_OK:
         raise PkvError("pkv_decode_step_host_pipelined", st)
     return out_host
+
+
+from .operators import (  # noqa: E402  (they use the binding above)
+    paged_decode_attention_fp8_block, paged_decode_attention_scored, rope_kv_append,
+    rope_kv_append_fp8_block, rotary_turns, workspace_size_scored)

@@ -18,6 +18,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libpkv.so")
 SOURCES = ["api.cu", "kv_append.cu", "copy_blocks.cu", "paged_decode.cu", "paged_decode_umma.cu",
            "static_scratch.cu",
+           "rope_append.cu", "paged_scored.cu", "ops_api.cu",
            "host_step.cu", "block_manager.cpp", "query_plan.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
