@@ -1,5 +1,6 @@
 // ops_api.cu -- the extern "C" entry points of include/pkv_ops.h: host checks,
 // plans, tensor maps and launches.
+#include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
 
@@ -39,6 +40,45 @@ cudaError_t device_limits(DeviceLimits *out)
     }
     *out = d;
     return cudaSuccess;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// A pool as boxes of one block's 16 tokens of `heads` kv heads, in shared memory
+// [head][128-byte column half][token][128 bytes] with the 128-byte swizzle: bf16
+// (64-element columns) or E4M3 codes (one 128-byte row per head).
+bool encode_pool(CUtensorMap *map, const void *base, int64_t num_blocks, int Hkv, int D, int heads,
+                 bool fp8)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode)
+        return false;
+    const cuuint64_t size = fp8 ? 1 : 2, cols = 128 / size;
+    const cuuint64_t halves = cuuint64_t(D) / cols, head = cuuint64_t(D) * size;
+    const cuuint64_t token = head * Hkv;
+    const cuuint64_t dims[5] = {cols, 16, halves, cuuint64_t(Hkv), cuuint64_t(num_blocks)};
+    const cuuint64_t strides[4] = {token, 128, head, 16 * token};
+    const cuuint32_t box[5] = {cuuint32_t(cols), 16, cuuint32_t(halves), cuuint32_t(heads), 1};
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                  const_cast<void *>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ------------------------------------------------------------------ rotation + append
@@ -138,6 +178,10 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
         return PKV_ERR_UNSUPPORTED;
     if (workspace_bytes < pl.ws_bytes)
         return PKV_ERR_WORKSPACE;
+    CUtensorMap kmap, vmap;
+    if (!encode_pool(&kmap, k_cache, num_blocks, Hkv, D, pl.HG, fp8) ||
+        !encode_pool(&vmap, v_cache, num_blocks, Hkv, D, pl.HG, fp8))
+        return PKV_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     pkv::ScoredParams p;
     memset(&p, 0, sizeof p);
@@ -169,10 +213,13 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.slopes = slopes;
-    p.softcap = softcap;
-    p.scale = scale;
-    p.window = window;
-    return pkv::launch_scored(pl, p, k_cache, v_cache, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    constexpr float kLog2e = 1.4426950408889634f;
+    p.mul = softcap > 0.f ? 2.f * scale * kLog2e / softcap : scale * kLog2e;
+    p.cap_log2 = softcap * kLog2e;
+    // a window that reaches back over the longest possible context hides nothing
+    p.window = int64_t(window) >= int64_t(max_blocks_per_seq) * pkv::kBlockSize ? 0 : window;
+    p.scale_vec = fp8 && pl.HG == 8 && aligned(k_scale, 8) && aligned(v_scale, 8);
+    return pkv::launch_scored(pl, p, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
 }

@@ -1,12 +1,42 @@
 // paged_scored.cu -- paged decode attention with capped scores, a distance bias or
 // a sliding window, over bf16 or block-scaled E4M3 pools.
 //
-// The simplest form: one CTA per (sequence, kv head) walks the sequence's blocks;
-// scores, softmax statistics and the accumulator live in shared memory in fp32.
+// Mathematics. For query j of a sequence of T tokens at position p = T - nq + j,
+//   x_t = cap(scale <q, k_t>) + slope (t - p),  out = sum_t 2^(y_t - m) v_t / sum_t 2^(y_t - m),
+// y = x log2(e), over p - window < t <= p, with a running maximum m (raised only when
+// a score passes it by more than a fixed lead; exact, since the sum uses the same m).
+// cap(z) = c tanh(z / c) = c (1 - 2 / (1 + 2^(2 z log2(e) / c))): one ex2 and one
+// reciprocal, absolute error 2^-22 c.
+//
+// Work. One unit is a 16-token block of a group of HG kv heads. The units of all
+// sequences (from the first block that any of the sequence's windows touches) lie
+// end to end; the persistent grid cuts them into equal cells, one per CTA. A
+// sequence inside one cell is finished in place; one cut by a cell's border leaves
+// its partial (m, l, acc) in the workspace for the merge kernel. The cells depend on
+// the sizes only, so results are deterministic.
+//
+// Staging. The last warp brings whole blocks of the group's heads by TMA (one box
+// for K, one for V: whole rows of the pool, contiguous where HG is all heads) into a
+// ring of shared-memory stages; the other warps consume, one kv head each (two or
+// four warps a head above 16 rows).
+//
+// E4M3 pools. The tensor cores multiply the codes as they are (mma.sync m16n8k32,
+// e4m3 x e4m3, fp32 sums): converting them to 16 bits first costs more issue slots
+// than everything else together, and the E4M3 product runs at 3.7 times the 16-bit
+// rate (measured: 1.15 against 2.14 cycles a warp instruction and SM, at twice the
+// depth). A query row is scaled by a power of two and held as hi + lo / 16, both
+// E4M3: bf16's 8 significant bits are exactly two E4M3 significands, so only
+// elements below 2^-12 of the row's largest lose bits. A softmax weight, times its
+// block's value scale over the row's largest so far and 2^6, is held the same way
+// (relative error at most 2^-8). hi and lo are two columns of one product; the two
+// are added when a score or an output is read. A block's key scale multiplies its
+// scores.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "pkv_cells.cuh"
 #include "pkv_common.cuh"
 #include "pkv_ops_internal.h"
 
@@ -14,148 +44,888 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr unsigned kFull = 0xffffffffu;
 
-__device__ __forceinline__ float e4m3_value(uint8_t c)
+// One stage's block: which sequence and logical block, what part it plays in its
+// segment (F_*), and the scale bytes of its heads.
+struct Header {
+    int32_t s, b, T, hg;
+    int32_t flags, cell, slot, unused;
+    uint8_t ks[8], vs[8];
+};
+static_assert(sizeof(Header) == 48, "three 16-byte words");
+
+struct Ring {
+    uint8_t *stages;
+    Header *hdr;
+    uint64_t *full, *empty;
+};
+
+__device__ __forceinline__ Ring carve(uint8_t *raw, const DecodeParams &d)
 {
-    uint32_t lo, hi;
-    e4m3x4_to_f16x2x2(c, lo, hi);
-    float f;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(lo));
-    return f;
+    uint8_t *base =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Ring r;
+    r.stages = base;
+    r.hdr = reinterpret_cast<Header *>(base + size_t(d.nst) * d.stage_bytes);
+    r.full = reinterpret_cast<uint64_t *>(r.hdr + d.nst);
+    r.empty = r.full + d.nst;
+    return r;
 }
 
-__global__ void __launch_bounds__(kThreads) scored_simple_kernel(const ScoredParams p, const void *kc,
-                                                                 const void *vc, int D)
+// Position in the ring.
+struct Turn {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next(int nst)
+    {
+        if (++st == uint32_t(nst)) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+struct Span {
+    int T;   // tokens (clamped to the table)
+    int b0;  // first block that a query's window touches
+    int nb;  // blocks from there
+};
+
+__device__ __forceinline__ int first_seen(const ScoredParams &p, int T)
 {
-    extern __shared__ float sm[];
+    const int f = T - p.d.nq - p.window + 1;
+    return p.window > 0 && f > 0 ? f : 0;
+}
+
+__device__ __forceinline__ Span span(const ScoredParams &p, int s)
+{
+    Span r;
+    r.T = seq_tokens(p.d, s);
+    r.b0 = first_seen(p, r.T) / kBlockSize;
+    r.nb = (r.T + kBlockSize - 1) / kBlockSize - r.b0;
+    return r;
+}
+
+// 2^e; 0 below the normal range.
+__device__ __forceinline__ float two_to(int e)
+{
+    return e < -126 ? 0.f : __uint_as_float(uint32_t(e + 127) << 23);
+}
+
+// ------------------------------------------------------------------ producer
+template <bool FP8>
+__device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const ScoredParams &p,
+                         const Ring &ring, int lane)
+{
     const DecodeParams &d = p.d;
-    const int R = d.rows, s = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    float *q = sm, *acc = q + R * D, *k = acc + R * D, *v = k + 16 * D, *x = v + 16 * D;
-    float *m = x + R * 16, *l = m + R, *corr = l + R;
-    int T = d.context_lens[s];
-    T = min(max(T, 0), d.MB * kBlockSize);
-    for (int e = tid; e < R * D; e += kThreads) {
-        const int row = e / D, j = row / d.G, g = row - j * d.G;
-        q[e] = __uint_as_float(uint32_t(d.q[((int64_t(s) * d.nq + j) * d.Hq + h * d.G + g) * D + e % D]) << 16);
-        acc[e] = 0.f;
+    const int S = d.S;
+    int64_t total = 0;
+    for (int s = lane; s < S; s += 32)
+        total += span(p, s).nb;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        total += __shfl_xor_sync(kFull, total, o);
+    Cells C;
+    C.F = C.F1 = int64_t(d.n_hg) * total;
+    C.F2 = 0;
+    C.G = int(gridDim.x);
+    C.NT = 0;
+    if (blockIdx.x == 0 && lane == 0) {
+        d.ws[kWsUnits] = uint32_t(total);
+        d.ws[kWsDense] = C.F >= C.G ? 1u : 0u;
     }
-    for (int r = tid; r < R; r += kThreads) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-    }
-    const int first = p.window ? max(0, T - d.nq - p.window + 1) : 0;
-    for (int b = first / kBlockSize; b * kBlockSize < T; ++b) {
-        const int phys = d.block_tables[int64_t(s) * d.MB + b];
-        const bool ok = phys >= 0 && phys < d.num_blocks;
-        if (!ok && tid == 0)
-            atomicOr(d.ws, kErrBadBlock);
-        __syncthreads();
-        for (int e = tid; e < 16 * D; e += kThreads) {
-            const int t = b * kBlockSize + e / D;
-            const int64_t at = ((int64_t(phys) * kBlockSize + e / D) * d.Hkv + h) * D + e % D;
-            float kv = 0.f, vv = 0.f;
-            if (ok && t < T && t >= first) {
-                if (p.k_scale) {
-                    const int64_t sc = int64_t(phys) * d.Hkv + h;
-                    kv = ldexpf(e4m3_value(static_cast<const uint8_t *>(kc)[at]), int(p.k_scale[sc]) - 127);
-                    vv = ldexpf(e4m3_value(static_cast<const uint8_t *>(vc)[at]), int(p.v_scale[sc]) - 127);
-                } else {
-                    kv = __uint_as_float(uint32_t(static_cast<const uint16_t *>(kc)[at]) << 16);
-                    vv = __uint_as_float(uint32_t(static_cast<const uint16_t *>(vc)[at]) << 16);
+    const int64_t a = C.start(blockIdx.x), e = C.start(int64_t(blockIdx.x) + 1);
+    Turn turn;
+    uint32_t issued = 0;
+    bool ok = true;
+
+    // wait until the next stage is free
+    auto acquire = [&]() -> bool {
+        if (issued < uint32_t(d.nst))
+            return true;
+        int w = 1;
+        if (lane == 0)
+            w = mbar_wait(smem_u32(&ring.empty[turn.st]), turn.phase ^ 1u, kWaitLimitNs);
+        return __shfl_sync(kFull, w, 0) != 0;
+    };
+
+    if (a < e) {
+        int hg = int(a / total);
+        int64_t rest = a - int64_t(hg) * total;
+        // the sequence that holds unit `rest` of its head group
+        int s = 0;
+        Span sp{0, 0, 0};
+        int b = 0;
+        for (int s0 = 0; s0 < S; s0 += 32) {
+            const int mine = s0 + lane < S ? span(p, s0 + lane).nb : 0;
+            int64_t incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o)
+                    incl += v;
+            }
+            const unsigned past = __ballot_sync(kFull, incl > rest);
+            if (past) {
+                const int src = __ffs(past) - 1;
+                s = s0 + src;
+                b = int(rest - __shfl_sync(kFull, incl - mine, src));
+                break;
+            }
+            rest -= __shfl_sync(kFull, incl, 31);
+        }
+        sp = span(p, s);
+        b += sp.b0;
+        const uint64_t policy = policy_evict_first();
+        const bool vec = FP8 && p.scale_vec;
+        bool opens = true;        // no segment of this cell ended yet
+        int seg_b0 = b;           // the segment's first block
+        int tab = -(1 << 30);     // first of the 32 table entries held by the lanes
+        int phys = 0;
+        uint2 ks = make_uint2(0, 0), vs = make_uint2(0, 0);
+        for (int64_t u = a; u < e; ++u) {
+            const int b_end = sp.b0 + sp.nb;
+            if (b >= tab + 32 || b < tab) {
+                tab = b;
+                phys = b + lane < b_end ? __ldg(d.block_tables + int64_t(s) * d.MB + b + lane) : 0;
+                if (phys < 0 || phys >= d.num_blocks) {
+                    atomicOr(d.ws + kWsErr, kErrBadBlock);
+                    phys = int(d.num_blocks);  // past the tensor's end: zeros
+                }
+                if (FP8) {
+                    // the scale bytes of the lane's block (the smallest scale for no block)
+                    ks = vs = make_uint2(0x01010101u, 0x01010101u);
+                    if (phys < d.num_blocks) {
+                        const int64_t at = int64_t(phys) * d.Hkv + hg * d.HG;
+                        if (vec) {
+                            ks = __ldg(reinterpret_cast<const uint2 *>(p.k_scale + at));
+                            vs = __ldg(reinterpret_cast<const uint2 *>(p.v_scale + at));
+                        } else {
+                            uint64_t kw = 0, vw = 0;
+                            for (int h = d.HG - 1; h >= 0; --h) {
+                                kw = kw << 8 | __ldg(p.k_scale + at + h);
+                                vw = vw << 8 | __ldg(p.v_scale + at + h);
+                            }
+                            ks = make_uint2(uint32_t(kw), uint32_t(kw >> 32));
+                            vs = make_uint2(uint32_t(vw), uint32_t(vw >> 32));
+                        }
+                    }
                 }
             }
-            k[e] = kv;
-            v[e] = vv;
-        }
-        __syncthreads();
-        for (int e = tid; e < R * 16; e += kThreads) {
-            const int row = e / 16, t = b * kBlockSize + e % 16, j = row / d.G;
-            const int pos = T - d.nq + j;
-            float y = 0.f;
-            for (int c = 0; c < D; ++c)
-                y = fmaf(q[row * D + c], k[(e % 16) * D + c], y);
-            y *= p.scale;
-            if (p.softcap > 0.f)
-                y = p.softcap * tanhf(y / p.softcap);
-            if (p.slopes)
-                y += p.slopes[h * d.G + row - j * d.G] * float(t - pos);
-            const bool seen = t <= pos && (!p.window || t > pos - p.window);
-            x[e] = seen ? y : -INFINITY;
-        }
-        __syncthreads();
-        for (int r = tid; r < R; r += kThreads) {
-            float top = m[r];
-            for (int c = 0; c < 16; ++c)
-                top = fmaxf(top, x[r * 16 + c]);
-            const float mu = top == -INFINITY ? 0.f : top;
-            corr[r] = expf(m[r] - mu);
-            float sum = 0.f;
-            for (int c = 0; c < 16; ++c) {
-                x[r * 16 + c] = expf(x[r * 16 + c] - mu);
-                sum += x[r * 16 + c];
+            const int src = b - tab;
+            const int block = __shfl_sync(kFull, phys, src);
+            uint4 scales = make_uint4(0, 0, 0, 0);
+            if (FP8) {
+                scales.x = __shfl_sync(kFull, ks.x, src);
+                scales.y = __shfl_sync(kFull, ks.y, src);
+                scales.z = __shfl_sync(kFull, vs.x, src);
+                scales.w = __shfl_sync(kFull, vs.y, src);
             }
-            l[r] = l[r] * corr[r] + sum;
-            m[r] = top;
-        }
-        __syncthreads();
-        for (int e = tid; e < R * D; e += kThreads) {
-            float a = acc[e] * corr[e / D];
-            for (int c = 0; c < 16; ++c)
-                a = fmaf(x[e / D * 16 + c], v[c * D + e % D], a);
-            acc[e] = a;
+            const bool first = u == a || b == sp.b0;
+            if (first)
+                seg_b0 = b;
+            const bool ends = b == b_end - 1, last = u == e - 1 || ends;
+            if (!(ok = acquire()))
+                break;
+            if (lane == 0) {
+                // the merge's record: cell (and slot) of the sequence's first piece,
+                // cell of its last
+                int2 *rec = d.pieces + int64_t(s) * d.n_hg + hg;
+                if (b == sp.b0)
+                    rec->x = int(blockIdx.x) * 2 + (opens ? 0 : 1);
+                if (ends)
+                    rec->y = int(blockIdx.x);
+                const int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) |
+                                  (last && ends && seg_b0 == sp.b0 ? F_DIRECT : 0);
+                int4 *h = reinterpret_cast<int4 *>(&ring.hdr[turn.st]);
+                h[0] = make_int4(s, b, sp.T, hg);
+                h[1] = make_int4(flags, int(blockIdx.x), opens ? 0 : 1, 0);
+                if (FP8)
+                    reinterpret_cast<uint4 *>(h)[2] = scales;
+                const uint32_t bar = smem_u32(&ring.full[turn.st]);
+                mbar_arrive_expect_tx(bar, uint32_t(d.stage_bytes));
+                const uint32_t dst = smem_u32(ring.stages + size_t(turn.st) * d.stage_bytes);
+                tma_load_5d_hint(dst, kmap, bar, 0, 0, 0, hg * d.HG, block, policy);
+                tma_load_5d_hint(dst + uint32_t(d.stage_bytes / 2), vmap, bar, 0, 0, 0, hg * d.HG,
+                                 block, policy);
+            }
+            __syncwarp();
+            ++issued;
+            turn.next(d.nst);
+            if (last)
+                opens = false;
+            if (++b == b_end && u + 1 < e) {
+                do {
+                    if (++s == S) {
+                        s = 0;
+                        ++hg;
+                    }
+                    sp = span(p, s);
+                } while (sp.nb == 0);
+                b = sp.b0;
+                tab = -(1 << 30);
+            }
         }
     }
+    if (ok && (ok = acquire()) && lane == 0) {
+        ring.hdr[turn.st].flags = F_END;
+        mbar_arrive(smem_u32(&ring.full[turn.st]));
+    }
+    if (!ok && lane == 0) {
+        atomicOr(d.ws + kWsErr, kErrProducerWait);
+        // wait (bounded) for every copy that may still be in flight
+        const uint32_t n = issued < uint32_t(d.nst) ? issued : uint32_t(d.nst);
+        for (uint32_t k = 0; k < n; ++k) {
+            if (turn.st == 0) {
+                turn.st = uint32_t(d.nst);
+                turn.phase ^= 1u;
+            }
+            --turn.st;
+            if (!mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs))
+                atomicOr(d.ws + kWsErr, kErrDrainWait);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ consumers
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x - value(code) of two packed E4M3 codes.
+__device__ __forceinline__ void residual2(uint16_t codes, float x0, float x1, float &r0, float &r1)
+{
+    float h0, h1;
+    asm("{\n\t.reg .b32 w;\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.f16x2.e4m3x2 w, %2;\n\t"
+        "mov.b32 {lo, hi}, w;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t"
+        "cvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(h0), "=f"(h1)
+        : "h"(codes));
+    r0 = x0 - h0;
+    r1 = x1 - h1;
+}
+
+constexpr float kLo = 16.f;        // scale of the lo terms
+constexpr int kWeightBits = 6;     // weights are scaled by 2^6 (at most 2^2 before it)
+constexpr float kLeadFp8 = 2.f;    // log2: so hi stays at or under 256 of E4M3's 448
+constexpr float kLeadBf16 = 8.f;
+
+// The rows of a warp. bf16: NT n-tiles of 8 rows, a lane holding rows 2 tq and
+// 2 tq + 1 of each; E4M3: NT n-tiles of 4 rows (hi and lo columns side by side), a
+// lane holding row tq of each. Either way rows x tokens g and g + 8.
+template <int D, bool FP8, int NT, int WPH>
+__device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane)
+{
+    constexpr int RN = FP8 ? 4 : 8;      // rows of an n-tile
+    constexpr int RL = FP8 ? NT : 2 * NT;  // rows of a lane
+    constexpr int BL = FP8 ? 2 : 1;      // blocks of a step
+    constexpr int NH = FP8 ? 1 : D / 64;
+    constexpr int KS = FP8 ? D / 32 : D / 16;
+    constexpr int MT = D / 16;
+    constexpr float kLead = FP8 ? kLeadFp8 : kLeadBf16;
+    const DecodeParams &d = p.d;
+    const int hl = cw / WPH, r0 = (cw % WPH) * RN * NT;
+    const int g = lane >> 2, tq = lane & 3;
+    // ldmatrix rows inside a [16 tokens][8 x 16 bytes] tile, 128-byte swizzle
+    const int k_tok = (lane & 7) + ((lane >> 3) & 1) * 8, k_chunk = lane >> 4;
+    const int v_tok = (lane & 7) + ((lane >> 4) & 1) * 8, v_chunk = (lane >> 3) & 1;
+    const int sw = lane & 7;
+
+    uint32_t qf[NT][KS][2];
+    float acc[MT][NT][4];
+    float m_r[RL], l_r[RL], mul[RL], slope[RL];
+    int row_j[RL];  // query index of each row (the last one for rows past the end)
+    int e_max = 0;  // E4M3: the largest value-scale byte so far
+#pragma unroll
+    for (int i = 0; i < RL; ++i) {
+        const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
+        const int j = row / d.G;
+        row_j[i] = j < d.nq ? j : d.nq - 1;
+        slope[i] = 0.f;
+        mul[i] = p.mul;
+    }
+    const uint32_t stages = smem_u32(ring.stages);
+    Turn turn;
+    for (;;) {
+        bool up = mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs);
+        const Header *h = &ring.hdr[turn.st];
+        const int flags = up ? h->flags : F_END;
+        // E4M3: the next block of the same segment goes along (the depth of one product
+        // is 32 tokens)
+        Turn turn2 = turn;
+        turn2.next(d.nst);
+        const bool two = BL == 2 && !(flags & (F_LAST | F_END));
+        if (two)
+            up = mbar_wait(smem_u32(&ring.full[turn2.st]), turn2.phase, kWaitLimitNs);
+        if (!up) {
+            if (lane == 0)
+                atomicOr(d.ws + kWsErr, kErrConsumerWait);
+            return;
+        }
+        if (flags & F_END)
+            break;
+        const Header *hb = two ? &ring.hdr[turn2.st] : h;
+        const int s = h->s, T = h->T, b = h->b, kvh = h->hg * d.HG + hl;
+        const int end_flags = hb->flags, e_cell = h->cell, e_slot = h->slot;
+
+        if (flags & F_FIRST) {
+            // ---- a new segment: empty state, its queries
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                m_r[i] = -INFINITY;
+                l_r[i] = 0.f;
+                if (p.slopes) {
+                    const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
+                    const int j = row / d.G;
+                    slope[i] = row < d.rows ? __ldg(p.slopes + kvh * d.G + row - j * d.G) *
+                                                  1.4426950408889634f
+                                            : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[i][nt][c] = 0.f;
+            e_max = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // column g of the tile: a row (bf16), or its hi or lo term
+                const int row = r0 + RN * nt + (FP8 ? g >> 1 : g);
+                const int j = row / d.G;
+                const bool valid = row < d.rows;
+                const uint16_t *q =
+                    d.q + ((int64_t(s) * d.nq + j) * d.Hq + int64_t(kvh) * d.G + row - j * d.G) * D;
+                if constexpr (FP8) {
+                    uint2 w[KS][2];
+                    float top = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            w[ks][c] = valid ? __ldg(reinterpret_cast<const uint2 *>(
+                                                   q + 32 * ks + 16 * c + 4 * tq))
+                                             : make_uint2(0, 0);
+                            top = fmaxf(top, fmaxf(fabsf(bf16lo_f32(w[ks][c].x)),
+                                                   fabsf(bf16hi_f32(w[ks][c].x))));
+                            top = fmaxf(top, fmaxf(fabsf(bf16lo_f32(w[ks][c].y)),
+                                                   fabsf(bf16hi_f32(w[ks][c].y))));
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                    // the row's largest element comes to 128 .. 256
+                    int e = int(__float_as_uint(top) >> 23) - 127 - 7;
+                    e = top == 0.f ? 0 : max(e, -119);
+                    const float f = two_to(-e);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t out = 0;
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t pair = x ? w[ks][c].y : w[ks][c].x;
+                                const float a = bf16lo_f32(pair) * f, bb = bf16hi_f32(pair) * f;
+                                uint16_t code = pack_e4m3x2(a, bb);
+                                if (g & 1) {
+                                    float ra, rb;
+                                    residual2(code, a, bb, ra, rb);
+                                    code = pack_e4m3x2(ra * kLo, rb * kLo);
+                                }
+                                out |= uint32_t(code) << (16 * x);
+                            }
+                            qf[nt][ks][c] = out;
+                        }
+                    // the factor of the lane's own row: from the column that holds it; not
+                    // a number where the row holds an infinity
+                    const float back = e > 120 ? NAN : two_to(e);
+                    mul[nt] = p.mul * __shfl_sync(kFull, back, (2 * tq) * 4);
+                } else {
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        qf[nt][ks][0] = valid ? __ldg(w + ks * 8 + tq) : 0u;
+                        qf[nt][ks][1] = valid ? __ldg(w + ks * 8 + 4 + tq) : 0u;
+                    }
+                }
+            }
+        }
+
+        // ---- scores S^T[token][row]
+        float sc[BL][NT][4];
+#pragma unroll
+        for (int k = 0; k < BL; ++k) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    sc[k][nt][c] = 0.f;
+            if (k == 1 && !two)
+                break;
+            const uint32_t kb = stages + (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
+                                uint32_t(hl * NH * kTileBytes);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const int chunk = 2 * ks + k_chunk;
+                uint32_t a[4];
+                ldsm_x4(kb + uint32_t((chunk >> 3) * kTileBytes + k_tok * 128 +
+                                      (((chunk & 7) ^ sw) << 4)),
+                        a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (FP8)
+                        mma_e4m3_16832(sc[k][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                    else
+                        mma_bf16_16816(sc[k][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                }
+            }
+        }
+
+        // ---- into y = x log2(e): x[k][i][c] is row i, block k, token g + 8 c
+        float x[BL][RL][2];
+        bool lead = false;
+        const int t0 = b * kBlockSize;
+        const int first = first_seen(p, T);
+        // blocks whose tokens are not all seen by all rows
+        const bool masked = t0 + BL * kBlockSize - 1 > T - d.nq ||
+                            (p.window > 0 && t0 < T - p.window);
+#pragma unroll
+        for (int k = 0; k < BL; ++k) {
+            const float kf = FP8 ? __uint_as_float(uint32_t((k ? hb : h)->ks[hl]) << 23) : 1.f;
+#pragma unroll
+            for (int i = 0; i < RL; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if constexpr (FP8)
+                        x[k][i][c] = fmaf(sc[k][i][2 * c + 1], 1.f / kLo, sc[k][i][2 * c]) * kf * mul[i];
+                    else
+                        x[k][i][c] = sc[k][i >> 1][2 * c + (i & 1)] * mul[i];
+                }
+        }
+        if (p.cap_log2 > 0.f) {
+#pragma unroll
+            for (int k = 0; k < BL; ++k)
+#pragma unroll
+                for (int i = 0; i < RL; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        x[k][i][c] = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(x[k][i][c])), p.cap_log2);
+        }
+        if (p.slopes) {
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                const float far = float(t0 + g - (T - d.nq + row_j[i]));
+#pragma unroll
+                for (int k = 0; k < BL; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        x[k][i][c] = fmaf(slope[i], far + float(16 * k + 8 * c), x[k][i][c]);
+            }
+        }
+        if (__builtin_expect(masked, 0)) {
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                const int pos = T - d.nq + row_j[i];
+                const int low = p.window > 0 ? pos - p.window : -1;  // the last one not seen
+#pragma unroll
+                for (int k = 0; k < BL; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int t = t0 + 16 * k + 8 * c + g;
+                        if (t > pos || t <= low)
+                            x[k][i][c] = -INFINITY;
+                    }
+            }
+        }
+        if (BL == 2 && !two) {
+#pragma unroll
+            for (int i = 0; i < RL; ++i)
+                x[BL - 1][i][0] = x[BL - 1][i][1] = -INFINITY;
+        }
+
+        // ---- running maximum; the accumulator follows it (and the largest value scale)
+        float top[RL];
+#pragma unroll
+        for (int i = 0; i < RL; ++i) {
+            top[i] = fmaxf(x[0][i][0], x[0][i][1]);
+            if (BL == 2)
+                top[i] = fmaxf(top[i], fmaxf(x[BL - 1][i][0], x[BL - 1][i][1]));
+            lead |= top[i] > m_r[i] + kLead;
+        }
+        int ev[2] = {0, 0}, e_new = 0;
+        if constexpr (FP8) {
+            ev[0] = h->vs[hl];
+            ev[1] = hb->vs[hl];
+            e_new = max(e_max, max(ev[0], ev[1]));
+        }
+        if (__any_sync(kFull, lead) || e_new > e_max) {
+            float corr[RL];
+            const float fe = FP8 ? two_to(e_max - e_new) : 1.f;
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                float t = top[i];
+                t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+                t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+                t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+                const float mn = fmaxf(m_r[i], t);
+                const float c = ex2(m_r[i] - (mn == -INFINITY ? 0.f : mn));
+                m_r[i] = mn;
+                l_r[i] *= c;
+                corr[i] = c * fe;
+            }
+            e_max = e_new;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[mt][nt][c] *= corr[FP8 ? nt : 2 * nt + (c & 1)];
+        }
+#pragma unroll
+        for (int i = 0; i < RL; ++i) {
+            const float mu = m_r[i] == -INFINITY ? 0.f : m_r[i];
+#pragma unroll
+            for (int k = 0; k < BL; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    x[k][i][c] = ex2(x[k][i][c] - mu);
+                    l_r[i] += x[k][i][c];
+                }
+        }
+
+        // ---- O^T[d][row] += V^T[d][token] P^T[token][row]; tokens that no row of the
+        //      sequence sees are zeroed in V too (stale slots may hold anything)
+        const bool edge = t0 < first || t0 + (two ? 32 : 16) > T;
+        if constexpr (FP8) {
+            // P as B fragments: bytes (token 2tq, 2tq + 8, 2tq + 1, 2tq + 9) of column g
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float f = two_to(ev[k] - e_max + kWeightBits);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float a = x[k][nt][0] * f, c = x[k][nt][1] * f;
+                    const uint16_t hi = pack_e4m3x2(a, c);
+                    float ra, rc;
+                    residual2(hi, a, c, ra, rc);
+                    const uint16_t lo = pack_e4m3x2(ra * kLo, rc * kLo);
+                    pb[nt][k] = movmatrix_trans(uint32_t(hi) | uint32_t(lo) << 16);
+                }
+            }
+            auto pv = [&](auto is_edge) {
+                constexpr bool EDGE = decltype(is_edge)::value;
+                uint32_t keep[2] = {kFull, kFull};
+                if constexpr (EDGE) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        keep[k] = 0u;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int t = t0 + 16 * k + 2 * tq + (c >> 1) + 8 * (c & 1);
+                            keep[k] |= t >= first && t < T ? 0xffu << (8 * c) : 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MT / 2; ++i) {
+                    uint32_t r[2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t vb = stages +
+                                            (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
+                                            uint32_t((d.HG + hl) * kTileBytes);
+                        if (k == 1 && !two)
+                            r[1][0] = r[1][1] = r[1][2] = r[1][3] = 0u;
+                        else
+                            ldsm_x4_trans(
+                                vb + uint32_t(v_tok * 128 + (((2 * i + v_chunk) ^ sw) << 4)), r[k]);
+                    }
+                    // m-tile 2i: dims 32i + 2g (and + 16 for rows g + 8), 2i + 1: + 1
+#pragma unroll
+                    for (int par = 0; par < 2; ++par) {
+                        const uint32_t sel = par ? 0x7351u : 0x6240u;
+                        uint32_t a[4] = {__byte_perm(r[0][0], r[0][2], sel),
+                                         __byte_perm(r[0][1], r[0][3], sel),
+                                         __byte_perm(r[1][0], r[1][2], sel),
+                                         __byte_perm(r[1][1], r[1][3], sel)};
+                        if constexpr (EDGE) {
+                            a[0] &= keep[0];
+                            a[1] &= keep[0];
+                            a[2] &= keep[1];
+                            a[3] &= keep[1];
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_e4m3_16832(acc[2 * i + par][nt], a, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            };
+            if (__builtin_expect(edge, 0))
+                pv(std::true_type());
+            else
+                pv(std::false_type());
+        } else {
+            // P = hi + lo (bf16 each), transposed into B fragments
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float a = x[0][2 * nt][c], bb = x[0][2 * nt + 1][c];
+                    const uint32_t hi = pack_bf16x2(a, bb);
+                    ph[nt][c] = movmatrix_trans(hi);
+                    pl[nt][c] = movmatrix_trans(pack_bf16x2(a - bf16lo_f32(hi), bb - bf16hi_f32(hi)));
+                }
+            auto pv = [&](auto is_edge) {
+                constexpr bool EDGE = decltype(is_edge)::value;
+                uint32_t keep[2] = {kFull, kFull};
+                if constexpr (EDGE) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int t = t0 + 8 * k + 2 * tq;
+                        keep[k] = (t >= first && t < T ? 0x0000ffffu : 0u) |
+                                  (t + 1 >= first && t + 1 < T ? 0xffff0000u : 0u);
+                    }
+                }
+                const uint32_t vb = stages + turn.st * uint32_t(d.stage_bytes) +
+                                    uint32_t((d.HG + hl) * NH * kTileBytes);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int chunk = 2 * i + v_chunk;
+                    uint32_t a[4];
+                    ldsm_x4_trans(vb + uint32_t((chunk >> 3) * kTileBytes + v_tok * 128 +
+                                                (((chunk & 7) ^ sw) << 4)),
+                                  a);
+                    if constexpr (EDGE) {
+                        a[0] &= keep[0];
+                        a[1] &= keep[0];
+                        a[2] &= keep[1];
+                        a[3] &= keep[1];
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16_16816(acc[i][nt], a, ph[nt][0], ph[nt][1]);
+                        mma_bf16_16816(acc[i][nt], a, pl[nt][0], pl[nt][1]);
+                    }
+                }
+            };
+            if (__builtin_expect(edge, 0))
+                pv(std::true_type());
+            else
+                pv(std::false_type());
+        }
+
+        // ---- the stages go back to the producer
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&ring.empty[turn.st]));
+            if (two)
+                mbar_arrive(smem_u32(&ring.empty[turn2.st]));
+        }
+        turn.next(d.nst);
+        if (two)
+            turn.next(d.nst);
+
+        if (end_flags & F_LAST) {
+            // ---- the segment's end: full row sums, then the output or a partial
+            const bool direct = end_flags & F_DIRECT;
+            const float vf = FP8 ? ldexpf(1.f, e_max - 127 - kWeightBits) : 1.f;
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                float l = l_r[i];
+                l += __shfl_xor_sync(kFull, l, 4);
+                l += __shfl_xor_sync(kFull, l, 8);
+                l += __shfl_xor_sync(kFull, l, 16);
+                const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
+                if (row >= d.rows)
+                    continue;
+                const int j = row / d.G;
+                const int64_t o =
+                    ((int64_t(s) * d.nq + j) * d.Hq + int64_t(kvh) * d.G + row - j * d.G) * D;
+                const int64_t part = ((int64_t(e_cell) * 2 + e_slot) * d.HG + hl) * d.rows + row;
+                const float f = (direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f) * vf;
+                if (!direct && g == 0)
+                    *reinterpret_cast<float2 *>(d.ml + part * 2) = make_float2(m_r[i], l);
+                float *pf = direct ? static_cast<float *>(d.out) + o : d.part + part * D;
+                const bool as_bf16 = direct && !d.out_f32;
+                __nv_bfloat16 *pb = static_cast<__nv_bfloat16 *>(d.out) + o;
+#pragma unroll
+                for (int mt = 0; mt < MT; mt += FP8 ? 2 : 1)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if constexpr (FP8) {
+                            // dims 2g, 2g + 1 of the chunk: the even and the odd m-tile
+                            const float v0 =
+                                fmaf(acc[mt][i][2 * c + 1], 1.f / kLo, acc[mt][i][2 * c]) * f;
+                            const float v1 =
+                                fmaf(acc[mt + 1][i][2 * c + 1], 1.f / kLo, acc[mt + 1][i][2 * c]) * f;
+                            const int dim = 16 * mt + 16 * c + 2 * g;
+                            if (as_bf16)
+                                *reinterpret_cast<uint32_t *>(pb + dim) = pack_bf16x2(v0, v1);
+                            else
+                                *reinterpret_cast<float2 *>(pf + dim) = make_float2(v0, v1);
+                        } else {
+                            const float v = acc[mt][i >> 1][2 * c + (i & 1)] * f;
+                            const int dim = 16 * mt + 8 * c + g;
+                            if (as_bf16)
+                                pb[dim] = __float2bfloat16_rn(v);
+                            else
+                                pf[dim] = v;
+                        }
+                    }
+            }
+        }
+    }
+}
+
+constexpr int kConsumers = 8;
+
+template <int D, bool FP8, int NT, int WPH>
+__global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
+    scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ ScoredParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const Ring ring = carve(smem_raw, p.d);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        for (int i = 0; i < p.d.nst; ++i) {
+            mbar_init(smem_u32(&ring.full[i]), 1);
+            mbar_init(smem_u32(&ring.empty[i]), uint32_t(p.d.ncw));
+        }
+        fence_mbar_init();
+    }
+    // the kernel before this one on the stream may still write q or the pools
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
-    for (int e = tid; e < R * D; e += kThreads) {
-        const int row = e / D, j = row / d.G, g = row - j * d.G;
-        const int64_t o = ((int64_t(s) * d.nq + j) * d.Hq + h * d.G + g) * D + e % D;
-        const float y = l[row] > 0.f ? acc[e] / l[row] : (l[row] == 0.f ? 0.f : l[row]);
-        if (d.out_f32)
-            static_cast<float *>(d.out)[o] = y;
-        else
-            static_cast<__nv_bfloat16 *>(d.out)[o] = __float2bfloat16_rn(y);
-    }
+    if (warp == p.d.ncw)
+        producer<FP8>(&kmap, &vmap, p, ring, lane);
+    else
+        consumer<D, FP8, NT, WPH>(p, ring, warp, lane);
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+template <int D, bool FP8, int NT, int WPH>
+cudaError_t launch_one(const DecodePlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
+                       const CUtensorMap &vmap, cudaStream_t stream)
+{
+    const auto kern = scored_kernel<D, FP8, NT, WPH>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(pl.smem));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(pl.grid));
+    cfg.blockDim = dim3(unsigned(pl.threads));
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_merge(pl, p.d, stream);
+}
 
 }  // namespace
 
 int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
                 int fp8, DecodePlan *pl)
 {
-    (void)MB;
-    (void)num_sms;
     DecodePlan P{};
     P.D = D;
     P.kv8 = fp8;
     P.G = Hq / Hkv;
     P.rows = P.G * nq;
-    P.HG = 1;
-    P.n_hg = Hkv;
-    P.wph = 1;
-    P.smem = size_t(2 * P.rows * D + 32 * D + P.rows * 19) * 4;
-    if (int(P.smem) > smem_optin || Hkv > 65535)
+    const int tile = fp8 ? 4 : 8;
+    const int tiles = (P.rows + tile - 1) / tile;
+    const int most = fp8 ? 4 : 2;  // n-tiles of a warp: 16 rows
+    P.ntw = tiles == 1 ? 1 : tiles == 2 ? 2 : most;
+    P.wph = tiles <= most ? 1 : tiles <= 2 * most ? 2 : 4;
+    P.rows_pad = P.wph * P.ntw * tile;
+    if (P.rows > P.rows_pad)
         return -1;
+    P.HG = 1;
+    for (int h = std::min(kConsumers / P.wph, Hkv); h >= 1; --h)
+        if (Hkv % h == 0) {
+            P.HG = h;
+            break;
+        }
+    P.n_hg = Hkv / P.HG;
+    P.threads = 32 * (1 + P.HG * P.wph);
+    P.stage_bytes = 2 * P.HG * (fp8 ? 1 : D / 64) * kTileBytes;
+    // few heads: several CTAs share an SM, so that as many warps hide each other's waits
+    P.ctas_per_sm = std::min(4, std::max(1, kConsumers / (P.HG * P.wph)));
+    const int per_stage = P.stage_bytes + int(sizeof(Header)) + 16;
+    const int budget = P.ctas_per_sm == 1 ? smem_optin : (smem_optin + 1024) / P.ctas_per_sm - 1024;
+    P.nst = std::min(16, (budget - 1024) / per_stage);
+    if (P.nst < 3)
+        return -1;
+    P.smem = 1024 + size_t(P.nst) * per_stage;
+    const int cap = P.ctas_per_sm * num_sms;
+    P.grid = int(std::min<int64_t>(cap, int64_t(P.n_hg) * S * MB));
     P.off_rec = kWsHeaderBytes;
     P.off_ml = P.off_rec + round_up(size_t(S) * P.n_hg * 8, 256);
-    P.off_part = P.off_ml;
-    P.ws_bytes = P.off_part;
+    P.off_part = P.off_ml + round_up(size_t(cap) * 2 * P.HG * P.rows * 2 * 4, 256);
+    P.ws_bytes = P.off_part + round_up(size_t(cap) * 2 * P.HG * P.rows * size_t(D) * 4, 256);
     *pl = P;
     return 0;
 }
 
-cudaError_t launch_scored(const DecodePlan &pl, const ScoredParams &p, const void *kc,
-                          const void *vc, cudaStream_t stream)
+cudaError_t launch_scored(const DecodePlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
+                          const CUtensorMap &vmap, cudaStream_t stream)
 {
-    cudaError_t e = cudaFuncSetAttribute(scored_simple_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(pl.smem));
-    if (e != cudaSuccess)
-        return e;
-    scored_simple_kernel<<<dim3(unsigned(p.d.S), unsigned(p.d.Hkv)), kThreads, pl.smem, stream>>>(
-        p, kc, vc, pl.D);
-    return cudaGetLastError();
+    if (pl.kv8) {
+        if (pl.wph == 4)
+            return launch_one<128, true, 4, 4>(pl, p, kmap, vmap, stream);
+        if (pl.wph == 2)
+            return launch_one<128, true, 4, 2>(pl, p, kmap, vmap, stream);
+        if (pl.ntw == 4)
+            return launch_one<128, true, 4, 1>(pl, p, kmap, vmap, stream);
+        if (pl.ntw == 2)
+            return launch_one<128, true, 2, 1>(pl, p, kmap, vmap, stream);
+        return launch_one<128, true, 1, 1>(pl, p, kmap, vmap, stream);
+    }
+    if (pl.D == 64) {
+        if (pl.wph == 4)
+            return launch_one<64, false, 2, 4>(pl, p, kmap, vmap, stream);
+        if (pl.wph == 2)
+            return launch_one<64, false, 2, 2>(pl, p, kmap, vmap, stream);
+        if (pl.ntw == 2)
+            return launch_one<64, false, 2, 1>(pl, p, kmap, vmap, stream);
+        return launch_one<64, false, 1, 1>(pl, p, kmap, vmap, stream);
+    }
+    if (pl.wph == 4)
+        return launch_one<128, false, 2, 4>(pl, p, kmap, vmap, stream);
+    if (pl.wph == 2)
+        return launch_one<128, false, 2, 2>(pl, p, kmap, vmap, stream);
+    if (pl.ntw == 2)
+        return launch_one<128, false, 2, 1>(pl, p, kmap, vmap, stream);
+    return launch_one<128, false, 1, 1>(pl, p, kmap, vmap, stream);
 }
 
 }  // namespace pkv

@@ -41,16 +41,17 @@ struct ScoredParams {
     const uint8_t *k_scale;  // [num_blocks][Hkv] scale bytes (null: bf16 pools)
     const uint8_t *v_scale;
     const float *slopes;     // [Hq] or null
-    float softcap;           // 0: none
-    float scale;
+    float mul;               // to the log2 domain: scale log2(e), or 2 scale log2(e) / softcap
+    float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
+    int scale_vec;           // the scale bytes of a block's heads are an aligned 8-byte word
 };
 
 // The plan of a scored call (fp8: block-scaled pools); 0, or -1 if unsupported.
 int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
                 int fp8, DecodePlan *plan);
 
-cudaError_t launch_scored(const DecodePlan &plan, const ScoredParams &p, const void *k_cache,
-                          const void *v_cache, cudaStream_t stream);
+cudaError_t launch_scored(const DecodePlan &plan, const ScoredParams &p, const CUtensorMap &kmap,
+                          const CUtensorMap &vmap, cudaStream_t stream);
 
 }  // namespace pkv
