@@ -154,11 +154,10 @@ pkv_status pkv_rope_kv_append_fp8_block(
  * Other arguments, limits, errors and the error word as
  * pkv_paged_decode_attention; scores, softmax statistics and sums are fp32, the
  * result deterministic. Over bf16 pools a softmax weight is held as two bf16 terms
- * (2^-16). Over E4M3 pools a query is held as two E4M3 terms (to 2^-20 of its
- * head row's largest element) and a weight as two as well (relative error at
- * most 2^-8, of either sign; steps of 2^-20 for the smallest): before the
- * output's rounding the error is at most 2^-8 of sum p |V_s| / sum p, and near
- * a tenth of that in the mean.
+ * (2^-16). Over E4M3 pools a query row is scaled by a power of two and held in
+ * f16 (exact but for elements below 2^-28 of its largest), and a weight as one f16
+ * term (2^-11): before the output's rounding the error is at most 2^-11 of
+ * sum p |V_s| / sum p beside the scores' own fp32 rounding.
  */
 size_t pkv_workspace_size_scored(int32_t num_seqs, int32_t n_query_per_seq, int32_t num_q_heads,
                                  int32_t num_kv_heads, int32_t head_dim);

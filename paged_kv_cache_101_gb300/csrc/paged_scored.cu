@@ -20,17 +20,19 @@
 // ring of shared-memory stages; the other warps consume, one kv head each (two or
 // four warps a head above 16 rows).
 //
-// E4M3 pools. The tensor cores multiply the codes as they are (mma.sync m16n8k32,
-// e4m3 x e4m3, fp32 sums): converting them to 16 bits first costs more issue slots
-// than everything else together, and the E4M3 product runs at 3.7 times the 16-bit
-// rate (measured: 1.15 against 2.14 cycles a warp instruction and SM, at twice the
-// depth). A query row is scaled by a power of two and held as hi + lo / 16, both
-// E4M3: bf16's 8 significant bits are exactly two E4M3 significands, so only
-// elements below 2^-12 of the row's largest lose bits. A softmax weight, times its
-// block's value scale over the row's largest so far and 2^6, is held the same way
-// (relative error at most 2^-8). hi and lo are two columns of one product; the two
-// are added when a score or an output is read. A block's key scale multiplies its
-// scores.
+// E4M3 pools. Codes become f16 (exact) on their way from shared memory to the tensor
+// cores. (mma.sync takes E4M3 operands too, but on sm_103a the compiler turns that
+// into the same conversions for every product and fp32 additions: 661 warp
+// instructions for two blocks of a head with 4 rows against about half of it here.)
+// A query row is scaled by a power of two and held in f16: bf16's 8 significant bits
+// fit, so only elements below 2^-28 of the row's largest lose bits. A softmax weight,
+// times its block's value scale over the row's largest so far, is held in f16
+// (relative error at most 2^-11, steps of 2^-31 of the largest weight for the
+// smallest). A block's key scale multiplies its scores.
+//
+// Order. A segment's blocks are taken from the newest to the oldest: weights tend to
+// fall with distance (a distance bias makes sure of it), so the running maximum
+// settles at once instead of rising all along.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -88,7 +90,7 @@ struct Turn {
 struct Span {
     int T;   // tokens (clamped to the table)
     int b0;  // first block that a query's window touches
-    int nb;  // blocks from there
+    int nb;  // blocks from there (taken from the last to the first)
 };
 
 __device__ __forceinline__ int first_seen(const ScoredParams &p, int T)
@@ -175,19 +177,19 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
             rest -= __shfl_sync(kFull, incl, 31);
         }
         sp = span(p, s);
-        b += sp.b0;
+        b = sp.b0 + sp.nb - 1 - b;  // the newest block comes first
         const uint64_t policy = policy_evict_first();
         const bool vec = FP8 && p.scale_vec;
         bool opens = true;        // no segment of this cell ended yet
-        int seg_b0 = b;           // the segment's first block
-        int tab = -(1 << 30);     // first of the 32 table entries held by the lanes
+        bool from_top = false;    // the segment opens its sequence
+        int tab = -1;             // newest of the 32 blocks whose table entries the lanes hold
         int phys = 0;
         uint2 ks = make_uint2(0, 0), vs = make_uint2(0, 0);
         for (int64_t u = a; u < e; ++u) {
-            const int b_end = sp.b0 + sp.nb;
-            if (b >= tab + 32 || b < tab) {
+            const int b_top = sp.b0 + sp.nb - 1;
+            if (b <= tab - 32 || tab < 0) {
                 tab = b;
-                phys = b + lane < b_end ? __ldg(d.block_tables + int64_t(s) * d.MB + b + lane) : 0;
+                phys = b - lane >= sp.b0 ? __ldg(d.block_tables + int64_t(s) * d.MB + b - lane) : 0;
                 if (phys < 0 || phys >= d.num_blocks) {
                     atomicOr(d.ws + kWsErr, kErrBadBlock);
                     phys = int(d.num_blocks);  // past the tensor's end: zeros
@@ -212,7 +214,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                     }
                 }
             }
-            const int src = b - tab;
+            const int src = tab - b;
             const int block = __shfl_sync(kFull, phys, src);
             uint4 scales = make_uint4(0, 0, 0, 0);
             if (FP8) {
@@ -221,22 +223,22 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                 scales.z = __shfl_sync(kFull, vs.x, src);
                 scales.w = __shfl_sync(kFull, vs.y, src);
             }
-            const bool first = u == a || b == sp.b0;
+            const bool first = u == a || b == b_top;
             if (first)
-                seg_b0 = b;
-            const bool ends = b == b_end - 1, last = u == e - 1 || ends;
+                from_top = b == b_top;
+            const bool ends = b == sp.b0, last = u == e - 1 || ends;
             if (!(ok = acquire()))
                 break;
             if (lane == 0) {
                 // the merge's record: cell (and slot) of the sequence's first piece,
                 // cell of its last
                 int2 *rec = d.pieces + int64_t(s) * d.n_hg + hg;
-                if (b == sp.b0)
+                if (b == b_top)
                     rec->x = int(blockIdx.x) * 2 + (opens ? 0 : 1);
                 if (ends)
                     rec->y = int(blockIdx.x);
                 const int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) |
-                                  (last && ends && seg_b0 == sp.b0 ? F_DIRECT : 0);
+                                  (ends && from_top ? F_DIRECT : 0);
                 int4 *h = reinterpret_cast<int4 *>(&ring.hdr[turn.st]);
                 h[0] = make_int4(s, b, sp.T, hg);
                 h[1] = make_int4(flags, int(blockIdx.x), opens ? 0 : 1, 0);
@@ -254,7 +256,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
             turn.next(d.nst);
             if (last)
                 opens = false;
-            if (++b == b_end && u + 1 < e) {
+            if (--b < sp.b0 && u + 1 < e) {
                 do {
                     if (++s == S) {
                         s = 0;
@@ -262,8 +264,8 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                     }
                     sp = span(p, s);
                 } while (sp.nb == 0);
-                b = sp.b0;
-                tab = -(1 << 30);
+                b = sp.b0 + sp.nb - 1;
+                tab = -1;
             }
         }
     }
@@ -288,16 +290,6 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
 }
 
 // ------------------------------------------------------------------ consumers
-__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ float rcp(float x)
 {
     float y;
@@ -305,41 +297,23 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
-// x - value(code) of two packed E4M3 codes.
-__device__ __forceinline__ void residual2(uint16_t codes, float x0, float x1, float &r0, float &r1)
-{
-    float h0, h1;
-    asm("{\n\t.reg .b32 w;\n\t.reg .b16 lo, hi;\n\t"
-        "cvt.rn.f16x2.e4m3x2 w, %2;\n\t"
-        "mov.b32 {lo, hi}, w;\n\t"
-        "cvt.f32.f16 %0, lo;\n\t"
-        "cvt.f32.f16 %1, hi;\n\t}"
-        : "=f"(h0), "=f"(h1)
-        : "h"(codes));
-    r0 = x0 - h0;
-    r1 = x1 - h1;
-}
+// log2 of what a weight may reach before the running maximum is raised
+constexpr float kLead = 8.f;
+// E4M3: weights are scaled by 2^6 (at most 2^14 with the lead; f16 ends at 2^16)
+constexpr int kWeightBits = 6;
 
-constexpr float kLo = 16.f;        // scale of the lo terms
-constexpr int kWeightBits = 6;     // weights are scaled by 2^6 (at most 2^2 before it)
-constexpr float kLeadFp8 = 2.f;    // log2: so hi stays at or under 256 of E4M3's 448
-constexpr float kLeadBf16 = 8.f;
-
-// The rows of a warp. bf16: NT n-tiles of 8 rows, a lane holding rows 2 tq and
-// 2 tq + 1 of each; E4M3: NT n-tiles of 4 rows (hi and lo columns side by side), a
-// lane holding row tq of each. Either way rows x tokens g and g + 8.
+// The rows of a warp: NT n-tiles of 8, a lane holding rows 2 tq and 2 tq + 1 of each,
+// tokens g and g + 8 of each of up to BL blocks.
 template <int D, bool FP8, int NT, int WPH>
 __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane)
 {
-    constexpr int RN = FP8 ? 4 : 8;      // rows of an n-tile
-    constexpr int RL = FP8 ? NT : 2 * NT;  // rows of a lane
-    constexpr int BL = FP8 ? 2 : 1;      // blocks of a step
+    constexpr int RL = 2 * NT;       // rows of a lane
+    constexpr int BL = FP8 ? 2 : 1;  // blocks of a step: two chains hide each other's waits
     constexpr int NH = FP8 ? 1 : D / 64;
-    constexpr int KS = FP8 ? D / 32 : D / 16;
-    constexpr int MT = D / 16;
-    constexpr float kLead = FP8 ? kLeadFp8 : kLeadBf16;
+    constexpr int KS = D / 16;       // k-steps of the scores
+    constexpr int MT = D / 16;       // 16-dim m-tiles of the output
     const DecodeParams &d = p.d;
-    const int hl = cw / WPH, r0 = (cw % WPH) * RN * NT;
+    const int hl = cw / WPH, r0 = (cw % WPH) * 8 * NT;
     const int g = lane >> 2, tq = lane & 3;
     // ldmatrix rows inside a [16 tokens][8 x 16 bytes] tile, 128-byte swizzle
     const int k_tok = (lane & 7) + ((lane >> 3) & 1) * 8, k_chunk = lane >> 4;
@@ -351,10 +325,10 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
     float m_r[RL], l_r[RL], mul[RL], slope[RL];
     int row_j[RL];  // query index of each row (the last one for rows past the end)
     int e_max = 0;  // E4M3: the largest value-scale byte so far
+    const auto row_of = [&](int i) { return r0 + 8 * (i >> 1) + 2 * tq + (i & 1); };
 #pragma unroll
     for (int i = 0; i < RL; ++i) {
-        const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
-        const int j = row / d.G;
+        const int j = row_of(i) / d.G;
         row_j[i] = j < d.nq ? j : d.nq - 1;
         slope[i] = 0.f;
         mul[i] = p.mul;
@@ -365,8 +339,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         bool up = mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs);
         const Header *h = &ring.hdr[turn.st];
         const int flags = up ? h->flags : F_END;
-        // E4M3: the next block of the same segment goes along (the depth of one product
-        // is 32 tokens)
+        // the next block of the same segment goes along
         Turn turn2 = turn;
         turn2.next(d.nst);
         const bool two = BL == 2 && !(flags & (F_LAST | F_END));
@@ -390,8 +363,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 m_r[i] = -INFINITY;
                 l_r[i] = 0.f;
                 if (p.slopes) {
-                    const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
-                    const int j = row / d.G;
+                    const int row = row_of(i), j = row / d.G;
                     slope[i] = row < d.rows ? __ldg(p.slopes + kvh * d.G + row - j * d.G) *
                                                   1.4426950408889634f
                                             : 0.f;
@@ -407,56 +379,42 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
             e_max = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                // column g of the tile: a row (bf16), or its hi or lo term
-                const int row = r0 + RN * nt + (FP8 ? g >> 1 : g);
+                const int row = r0 + 8 * nt + g;  // column g of the tile
                 const int j = row / d.G;
                 const bool valid = row < d.rows;
                 const uint16_t *q =
                     d.q + ((int64_t(s) * d.nq + j) * d.Hq + int64_t(kvh) * d.G + row - j * d.G) * D;
                 if constexpr (FP8) {
-                    uint2 w[KS][2];
+                    // k-step ks is 16-byte chunk ks of a code row: lane tq holds dims
+                    // 16 ks + 4 tq .. + 3 (k 2tq, 2tq + 1, 2tq + 8, 2tq + 9)
                     float top = 0.f;
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            w[ks][c] = valid ? __ldg(reinterpret_cast<const uint2 *>(
-                                                   q + 32 * ks + 16 * c + 4 * tq))
-                                             : make_uint2(0, 0);
-                            top = fmaxf(top, fmaxf(fabsf(bf16lo_f32(w[ks][c].x)),
-                                                   fabsf(bf16hi_f32(w[ks][c].x))));
-                            top = fmaxf(top, fmaxf(fabsf(bf16lo_f32(w[ks][c].y)),
-                                                   fabsf(bf16hi_f32(w[ks][c].y))));
-                        }
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const uint2 w = valid ? __ldg(reinterpret_cast<const uint2 *>(
+                                                    q + 16 * ks + 4 * tq))
+                                              : make_uint2(0, 0);
+                        qf[nt][ks][0] = w.x;
+                        qf[nt][ks][1] = w.y;
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo_f32(w.x)), fabsf(bf16hi_f32(w.x))),
+                                               fmaxf(fabsf(bf16lo_f32(w.y)), fabsf(bf16hi_f32(w.y)))));
+                    }
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-                    // the row's largest element comes to 128 .. 256
-                    int e = int(__float_as_uint(top) >> 23) - 127 - 7;
+                    // the row's largest element comes to 2^14 .. 2^15
+                    int e = int(__float_as_uint(top) >> 23) - 127 - 14;
                     e = top == 0.f ? 0 : max(e, -119);
                     const float f = two_to(-e);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t out = 0;
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t pair = x ? w[ks][c].y : w[ks][c].x;
-                                const float a = bf16lo_f32(pair) * f, bb = bf16hi_f32(pair) * f;
-                                uint16_t code = pack_e4m3x2(a, bb);
-                                if (g & 1) {
-                                    float ra, rb;
-                                    residual2(code, a, bb, ra, rb);
-                                    code = pack_e4m3x2(ra * kLo, rb * kLo);
-                                }
-                                out |= uint32_t(code) << (16 * x);
-                            }
-                            qf[nt][ks][c] = out;
-                        }
-                    // the factor of the lane's own row: from the column that holds it; not
-                    // a number where the row holds an infinity
-                    const float back = e > 120 ? NAN : two_to(e);
-                    mul[nt] = p.mul * __shfl_sync(kFull, back, (2 * tq) * 4);
+                        for (int c = 0; c < 2; ++c)
+                            qf[nt][ks][c] = pack_f16x2(bf16lo_f32(qf[nt][ks][c]) * f,
+                                                       bf16hi_f32(qf[nt][ks][c]) * f);
+                    // the factors of the lane's own rows; not a number where a row holds an
+                    // infinity (its products overflow f16)
+                    const float back = e > 113 ? NAN : two_to(e);
+                    mul[2 * nt] = p.mul * __shfl_sync(kFull, back, 8 * tq);
+                    mul[2 * nt + 1] = p.mul * __shfl_sync(kFull, back, 8 * tq + 4);
                 } else {
                     const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
 #pragma unroll
@@ -481,43 +439,52 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 break;
             const uint32_t kb = stages + (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
                                 uint32_t(hl * NH * kTileBytes);
+            if constexpr (FP8) {
+                // one ldmatrix brings chunks 2i and 2i + 1 of all 16 tokens
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int chunk = 2 * ks + k_chunk;
-                uint32_t a[4];
-                ldsm_x4(kb + uint32_t((chunk >> 3) * kTileBytes + k_tok * 128 +
-                                      (((chunk & 7) ^ sw) << 4)),
-                        a);
+                for (int i = 0; i < KS / 2; ++i) {
+                    uint32_t r[4], a0[4], a1[4];
+                    ldsm_x4(kb + uint32_t(k_tok * 128 + (((2 * i + k_chunk) ^ sw) << 4)), r);
+                    e4m3x4_to_f16x2x2(r[0], a0[0], a0[2]);
+                    e4m3x4_to_f16x2x2(r[1], a0[1], a0[3]);
+                    e4m3x4_to_f16x2x2(r[2], a1[0], a1[2]);
+                    e4m3x4_to_f16x2x2(r[3], a1[1], a1[3]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (FP8)
-                        mma_e4m3_16832(sc[k][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                    else
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16_16816(sc[k][nt], a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                        mma_f16_16816(sc[k][nt], a1, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const int chunk = 2 * ks + k_chunk;
+                    uint32_t a[4];
+                    ldsm_x4(kb + uint32_t((chunk >> 3) * kTileBytes + k_tok * 128 +
+                                          (((chunk & 7) ^ sw) << 4)),
+                            a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
                         mma_bf16_16816(sc[k][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
                 }
             }
         }
 
-        // ---- into y = x log2(e): x[k][i][c] is row i, block k, token g + 8 c
+        // ---- into y = x log2(e): x[k][i][c] is row i, block b - k, token g + 8 c
         float x[BL][RL][2];
-        bool lead = false;
-        const int t0 = b * kBlockSize;
+        const int t0 = b * kBlockSize;                          // the newer block
+        const int t_low = two ? t0 - kBlockSize : t0;           // the step's first token
         const int first = first_seen(p, T);
-        // blocks whose tokens are not all seen by all rows
-        const bool masked = t0 + BL * kBlockSize - 1 > T - d.nq ||
-                            (p.window > 0 && t0 < T - p.window);
+        // are all tokens of the step seen by all rows?
+        const bool masked = t0 + kBlockSize - 1 > T - d.nq || (p.window > 0 && t_low < T - p.window);
 #pragma unroll
         for (int k = 0; k < BL; ++k) {
             const float kf = FP8 ? __uint_as_float(uint32_t((k ? hb : h)->ks[hl]) << 23) : 1.f;
 #pragma unroll
             for (int i = 0; i < RL; ++i)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if constexpr (FP8)
-                        x[k][i][c] = fmaf(sc[k][i][2 * c + 1], 1.f / kLo, sc[k][i][2 * c]) * kf * mul[i];
-                    else
-                        x[k][i][c] = sc[k][i >> 1][2 * c + (i & 1)] * mul[i];
-                }
+                for (int c = 0; c < 2; ++c)
+                    x[k][i][c] = sc[k][i >> 1][2 * c + (i & 1)] * (FP8 ? kf * mul[i] : mul[i]);
         }
         if (p.cap_log2 > 0.f) {
 #pragma unroll
@@ -536,7 +503,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 for (int k = 0; k < BL; ++k)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        x[k][i][c] = fmaf(slope[i], far + float(16 * k + 8 * c), x[k][i][c]);
+                        x[k][i][c] = fmaf(slope[i], far + float(8 * c - 16 * k), x[k][i][c]);
             }
         }
         if (__builtin_expect(masked, 0)) {
@@ -548,7 +515,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 for (int k = 0; k < BL; ++k)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int t = t0 + 16 * k + 8 * c + g;
+                        const int t = t0 - 16 * k + 8 * c + g;
                         if (t > pos || t <= low)
                             x[k][i][c] = -INFINITY;
                     }
@@ -561,6 +528,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         }
 
         // ---- running maximum; the accumulator follows it (and the largest value scale)
+        bool lead = false;
         float top[RL];
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
@@ -597,7 +565,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        acc[mt][nt][c] *= corr[FP8 ? nt : 2 * nt + (c & 1)];
+                        acc[mt][nt][c] *= corr[2 * nt + (c & 1)];
         }
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
@@ -611,61 +579,78 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 }
         }
 
-        // ---- O^T[d][row] += V^T[d][token] P^T[token][row]; tokens that no row of the
-        //      sequence sees are zeroed in V too (stale slots may hold anything)
-        const bool edge = t0 < first || t0 + (two ? 32 : 16) > T;
-        if constexpr (FP8) {
-            // P as B fragments: bytes (token 2tq, 2tq + 8, 2tq + 1, 2tq + 9) of column g
-            uint32_t pb[NT][2];
+        // ---- O^T[d][row] += V^T[d][token] P^T[token][row], P transposed into B
+        //      fragments: bf16 as hi + lo, f16 (E4M3) with the block's value scale
+        uint32_t ph[BL][NT][2], pl[NT][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float f = two_to(ev[k] - e_max + kWeightBits);
+        for (int k = 0; k < BL; ++k) {
+            const float f = FP8 ? two_to(ev[k] - e_max + kWeightBits) : 1.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float a = x[k][nt][0] * f, c = x[k][nt][1] * f;
-                    const uint16_t hi = pack_e4m3x2(a, c);
-                    float ra, rc;
-                    residual2(hi, a, c, ra, rc);
-                    const uint16_t lo = pack_e4m3x2(ra * kLo, rc * kLo);
-                    pb[nt][k] = movmatrix_trans(uint32_t(hi) | uint32_t(lo) << 16);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float a = x[k][2 * nt][c], bb = x[k][2 * nt + 1][c];
+                    if constexpr (FP8) {
+                        ph[k][nt][c] = movmatrix_trans(pack_f16x2(a * f, bb * f));
+                    } else {
+                        const uint32_t hi = pack_bf16x2(a, bb);
+                        ph[k][nt][c] = movmatrix_trans(hi);
+                        pl[nt][c] = movmatrix_trans(
+                            pack_bf16x2(a - bf16lo_f32(hi), bb - bf16hi_f32(hi)));
+                    }
                 }
-            }
-            auto pv = [&](auto is_edge) {
-                constexpr bool EDGE = decltype(is_edge)::value;
+        }
+        // tokens that no row of the sequence sees are zeroed in V too (stale slots may
+        // hold anything)
+        const bool edge = t_low < first || t0 + kBlockSize > T;
+        auto pv = [&](auto is_edge) {
+            constexpr bool EDGE = decltype(is_edge)::value;
+#pragma unroll
+            for (int k = 0; k < BL; ++k) {
+                if (k == 1 && !two)
+                    break;
                 uint32_t keep[2] = {kFull, kFull};
                 if constexpr (EDGE) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        keep[k] = 0u;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int t = t0 + 16 * k + 2 * tq + (c >> 1) + 8 * (c & 1);
-                            keep[k] |= t >= first && t < T ? 0xffu << (8 * c) : 0u;
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        const int t = t0 - 16 * k + 8 * c + 2 * tq;
+                        keep[c] = (t >= first && t < T ? 0x0000ffffu : 0u) |
+                                  (t + 1 >= first && t + 1 < T ? 0xffff0000u : 0u);
                     }
                 }
+                const uint32_t vb = stages + (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
+                                    uint32_t((d.HG + hl) * NH * kTileBytes);
+                if constexpr (FP8) {
+                    // chunks 2i and 2i + 1: a lane gets tokens 2tq, 2tq + 1 of the code pair
+                    // (dims 2g, 2g + 1). Even dims (bytes 0, 2) make m-tile 2i, odd ones
+                    // m-tile 2i + 1; M-rows g + 8 are 16 dims on.
 #pragma unroll
-                for (int i = 0; i < MT / 2; ++i) {
-                    uint32_t r[2][4];
+                    for (int i = 0; i < MT / 2; ++i) {
+                        uint32_t r[4], ae[4], ao[4];
+                        ldsm_x4_trans(
+                            vb + uint32_t(v_tok * 128 + (((2 * i + v_chunk) ^ sw) << 4)), r);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t vb = stages +
-                                            (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
-                                            uint32_t((d.HG + hl) * kTileBytes);
-                        if (k == 1 && !two)
-                            r[1][0] = r[1][1] = r[1][2] = r[1][3] = 0u;
-                        else
-                            ldsm_x4_trans(
-                                vb + uint32_t(v_tok * 128 + (((2 * i + v_chunk) ^ sw) << 4)), r[k]);
+                        for (int m = 0; m < 4; ++m) {
+                            e4m3x4_to_f16x2x2(__byte_perm(r[m], 0u, 0x3120), ae[m], ao[m]);
+                            if constexpr (EDGE) {
+                                ae[m] &= keep[m >> 1];
+                                ao[m] &= keep[m >> 1];
+                            }
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16_16816(acc[2 * i][nt], ae, ph[k][nt][0], ph[k][nt][1]);
+                            mma_f16_16816(acc[2 * i + 1][nt], ao, ph[k][nt][0], ph[k][nt][1]);
+                        }
                     }
-                    // m-tile 2i: dims 32i + 2g (and + 16 for rows g + 8), 2i + 1: + 1
+                } else {
 #pragma unroll
-                    for (int par = 0; par < 2; ++par) {
-                        const uint32_t sel = par ? 0x7351u : 0x6240u;
-                        uint32_t a[4] = {__byte_perm(r[0][0], r[0][2], sel),
-                                         __byte_perm(r[0][1], r[0][3], sel),
-                                         __byte_perm(r[1][0], r[1][2], sel),
-                                         __byte_perm(r[1][1], r[1][3], sel)};
+                    for (int i = 0; i < MT; ++i) {
+                        const int chunk = 2 * i + v_chunk;
+                        uint32_t a[4];
+                        ldsm_x4_trans(vb + uint32_t((chunk >> 3) * kTileBytes + v_tok * 128 +
+                                                    (((chunk & 7) ^ sw) << 4)),
+                                      a);
                         if constexpr (EDGE) {
                             a[0] &= keep[0];
                             a[1] &= keep[0];
@@ -673,65 +658,18 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                             a[3] &= keep[1];
                         }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_e4m3_16832(acc[2 * i + par][nt], a, pb[nt][0], pb[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_bf16_16816(acc[i][nt], a, ph[k][nt][0], ph[k][nt][1]);
+                            mma_bf16_16816(acc[i][nt], a, pl[nt][0], pl[nt][1]);
+                        }
                     }
                 }
-            };
-            if (__builtin_expect(edge, 0))
-                pv(std::true_type());
-            else
-                pv(std::false_type());
-        } else {
-            // P = hi + lo (bf16 each), transposed into B fragments
-            uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float a = x[0][2 * nt][c], bb = x[0][2 * nt + 1][c];
-                    const uint32_t hi = pack_bf16x2(a, bb);
-                    ph[nt][c] = movmatrix_trans(hi);
-                    pl[nt][c] = movmatrix_trans(pack_bf16x2(a - bf16lo_f32(hi), bb - bf16hi_f32(hi)));
-                }
-            auto pv = [&](auto is_edge) {
-                constexpr bool EDGE = decltype(is_edge)::value;
-                uint32_t keep[2] = {kFull, kFull};
-                if constexpr (EDGE) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int t = t0 + 8 * k + 2 * tq;
-                        keep[k] = (t >= first && t < T ? 0x0000ffffu : 0u) |
-                                  (t + 1 >= first && t + 1 < T ? 0xffff0000u : 0u);
-                    }
-                }
-                const uint32_t vb = stages + turn.st * uint32_t(d.stage_bytes) +
-                                    uint32_t((d.HG + hl) * NH * kTileBytes);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int chunk = 2 * i + v_chunk;
-                    uint32_t a[4];
-                    ldsm_x4_trans(vb + uint32_t((chunk >> 3) * kTileBytes + v_tok * 128 +
-                                                (((chunk & 7) ^ sw) << 4)),
-                                  a);
-                    if constexpr (EDGE) {
-                        a[0] &= keep[0];
-                        a[1] &= keep[0];
-                        a[2] &= keep[1];
-                        a[3] &= keep[1];
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16_16816(acc[i][nt], a, ph[nt][0], ph[nt][1]);
-                        mma_bf16_16816(acc[i][nt], a, pl[nt][0], pl[nt][1]);
-                    }
-                }
-            };
-            if (__builtin_expect(edge, 0))
-                pv(std::true_type());
-            else
-                pv(std::false_type());
-        }
+            }
+        };
+        if (__builtin_expect(edge, 0))
+            pv(std::true_type());
+        else
+            pv(std::false_type());
 
         // ---- the stages go back to the producer
         __syncwarp();
@@ -754,7 +692,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 l += __shfl_xor_sync(kFull, l, 4);
                 l += __shfl_xor_sync(kFull, l, 8);
                 l += __shfl_xor_sync(kFull, l, 16);
-                const int row = r0 + (FP8 ? 4 * i + tq : 8 * (i >> 1) + 2 * tq + (i & 1));
+                const int row = row_of(i);
                 if (row >= d.rows)
                     continue;
                 const int j = row / d.G;
@@ -771,24 +709,21 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 for (int mt = 0; mt < MT; mt += FP8 ? 2 : 1)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+                        const float v0 = acc[mt][i >> 1][2 * c + (i & 1)] * f;
                         if constexpr (FP8) {
                             // dims 2g, 2g + 1 of the chunk: the even and the odd m-tile
-                            const float v0 =
-                                fmaf(acc[mt][i][2 * c + 1], 1.f / kLo, acc[mt][i][2 * c]) * f;
-                            const float v1 =
-                                fmaf(acc[mt + 1][i][2 * c + 1], 1.f / kLo, acc[mt + 1][i][2 * c]) * f;
+                            const float v1 = acc[mt + 1][i >> 1][2 * c + (i & 1)] * f;
                             const int dim = 16 * mt + 16 * c + 2 * g;
                             if (as_bf16)
                                 *reinterpret_cast<uint32_t *>(pb + dim) = pack_bf16x2(v0, v1);
                             else
                                 *reinterpret_cast<float2 *>(pf + dim) = make_float2(v0, v1);
                         } else {
-                            const float v = acc[mt][i >> 1][2 * c + (i & 1)] * f;
                             const int dim = 16 * mt + 8 * c + g;
                             if (as_bf16)
-                                pb[dim] = __float2bfloat16_rn(v);
+                                pb[dim] = __float2bfloat16_rn(v0);
                             else
-                                pf[dim] = v;
+                                pf[dim] = v0;
                         }
                     }
             }
@@ -861,14 +796,11 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     P.kv8 = fp8;
     P.G = Hq / Hkv;
     P.rows = P.G * nq;
-    const int tile = fp8 ? 4 : 8;
-    const int tiles = (P.rows + tile - 1) / tile;
-    const int most = fp8 ? 4 : 2;  // n-tiles of a warp: 16 rows
-    P.ntw = tiles == 1 ? 1 : tiles == 2 ? 2 : most;
-    P.wph = tiles <= most ? 1 : tiles <= 2 * most ? 2 : 4;
-    P.rows_pad = P.wph * P.ntw * tile;
-    if (P.rows > P.rows_pad)
-        return -1;
+    // up to 16 rows a warp
+    const int tiles = (P.rows + 7) / 8;
+    P.ntw = tiles == 1 ? 1 : 2;
+    P.wph = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
+    P.rows_pad = P.wph * P.ntw * 8;
     P.HG = 1;
     for (int h = std::min(kConsumers / P.wph, Hkv); h >= 1; --h)
         if (Hkv % h == 0) {
@@ -901,11 +833,9 @@ cudaError_t launch_scored(const DecodePlan &pl, const ScoredParams &p, const CUt
 {
     if (pl.kv8) {
         if (pl.wph == 4)
-            return launch_one<128, true, 4, 4>(pl, p, kmap, vmap, stream);
+            return launch_one<128, true, 2, 4>(pl, p, kmap, vmap, stream);
         if (pl.wph == 2)
-            return launch_one<128, true, 4, 2>(pl, p, kmap, vmap, stream);
-        if (pl.ntw == 4)
-            return launch_one<128, true, 4, 1>(pl, p, kmap, vmap, stream);
+            return launch_one<128, true, 2, 2>(pl, p, kmap, vmap, stream);
         if (pl.ntw == 2)
             return launch_one<128, true, 2, 1>(pl, p, kmap, vmap, stream);
         return launch_one<128, true, 1, 1>(pl, p, kmap, vmap, stream);

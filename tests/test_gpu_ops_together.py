@@ -104,9 +104,9 @@ class Server:
         sl = kw.get("slopes")
         ref, mag, big, low = R.attention(to_f64(q), k, v, tables, lens, nq, 1 / math.sqrt(D),
                                          kw.get("softcap", 0.0), sl, kw.get("window", 0), exps)
-        weight = (2.0 ** -8 if self.fp8 else 2.0 ** -16) + 2 * (big[..., None] * 2.0 ** -17
-                                                                + 2.0 ** -14) + 2.0 ** -20
-        assert (np.abs(to_f64(out) - ref) <= weight * mag + 2.0 ** -20 * low).all()
+        weight = (2.0 ** -11 if self.fp8 else 2.0 ** -16) + 2 * (big[..., None] * 2.0 ** -18
+                                                                 + 2.0 ** -14) + 2.0 ** -20
+        assert (np.abs(to_f64(out) - ref) <= weight * mag + 2.0 ** -31 * low).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True])

@@ -3,12 +3,12 @@
 
 Tolerance, with A = sum p |v| / sum p (the 64-bit reference with |v|): relative errors of
 the weights move the output by at most their size times A. They are
- - bf16 pools: 2^-16 (a weight in two bf16 terms); E4M3 pools: 2^-8 (two E4M3 terms), or
-   where that is more 2^-20 absolute for a weight times 2^(its value scale - the row's
-   largest value scale), the largest weight being 1 or more (the terms' smallest steps);
+ - bf16 pools: 2^-16 (a weight in two bf16 terms); E4M3 pools: 2^-11 (half a step of one f16), or
+   where that is more 2^-31 absolute for a weight times 2^(its value scale - the row's
+   largest value scale), the largest weight being 1 or more (f16's smallest step);
  - the score's absolute error, twice (numerator and sum): fp32 products and sums,
-   2^-18 * max sum |q||k| * scale; with E4M3 pools as much again for q's two terms; the
-   cap's tanh adds softcap * 2^-21, the distance bias |slope| * distance * 2^-22.
+   2^-18 * max sum |q||k| * scale; the cap's tanh adds softcap * 2^-21, the distance
+   bias |slope| * distance * 2^-22.
 Then 2^-20 A for fp32 sums over the context, and the rounding to bf16 (2^-8) where the
 output is bf16.
 """
@@ -102,15 +102,15 @@ class Batch:
             np.float64(np.float32(self.scale)), softcap, f32, window,
             v_exp=self.vs.astype(int) if self.fp8 else None)
         T = np.repeat(np.maximum(self.lens, 0), self.nq)[:, None]
-        score = big * 2.0 ** (-17 if self.fp8 else -18) + softcap * 2.0 ** -21
+        score = big * 2.0 ** -18 + softcap * 2.0 ** -21
         if slopes is not None:
             # distances that count: all for a bias that grows with it, else those whose
             # bias is over -100 (a weight of e^-100)
             near = 100 / np.maximum(np.abs(slopes), 1e-9)[None, :]
             reach = np.where(slopes[None, :] < 0, T, np.minimum(T, near))
             score = score + np.abs(slopes)[None, :] * reach * 2.0 ** -22
-        weight = (2.0 ** -8 if self.fp8 else 2.0 ** -16) + 2.0 ** -20 + 2 * score
-        bound = weight[..., None] * mag + 2.0 ** -20 * low
+        weight = (2.0 ** -11 if self.fp8 else 2.0 ** -16) + 2.0 ** -20 + 2 * score
+        bound = weight[..., None] * mag + 2.0 ** -31 * low
         if out.dtype == torch.bfloat16:
             bound = bound + 2.0 ** -8 * (np.abs(ref) + bound)
         got = to_f64(out)
@@ -197,7 +197,7 @@ def test_queries_of_extreme_size():
     k, v = b.values()
     ref, mag, _, low = R.attention(R.value(b.q), k, v, b.tables, b.lens, 1, 1.0,
                                    v_exp=b.vs.astype(int))
-    assert np.all(np.abs(out - ref) <= 2.0 ** -7 * mag + 2.0 ** -20 * low)
+    assert np.all(np.abs(out - ref) <= 2.0 ** -10 * mag + 2.0 ** -31 * low)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
