@@ -5,9 +5,11 @@ call links the shared library. Up-to-date outputs are not rebuilt.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ SOURCES = ["api.cu", "kv_append.cu", "copy_blocks.cu", "paged_decode.cu", "paged
            "static_scratch.cu",
            "rope_append.cu", "paged_scored.cu", "ops_api.cu",
            "host_step.cu", "block_manager.cpp", "query_plan.cpp"]
+MARSHAL = os.path.join(PKG, "_torch_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,6 +49,7 @@ def _deps() -> float:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and os.path.exists(LIBRARY) and os.path.getmtime(LIBRARY) >= _deps():
+        build_marshal()
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []
@@ -63,12 +67,40 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
         return r.stdout + r.stderr
 
-    with ThreadPoolExecutor(len(cmds)) as ex:
+    with ThreadPoolExecutor(len(cmds) + 1) as ex:
+        ex.submit(build_marshal, force)
         list(ex.map(run, cmds))
     tmp = LIBRARY + f".tmp{os.getpid()}"
     run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIBRARY)
     return LIBRARY
+
+
+def build_marshal(force: bool = False) -> str:
+    """The C++ argument marshaller of operators.py, against the installed torch. Without
+    it (no torch headers, another ABI) the Python face marshals by itself, more slowly:
+    a failure is reported, not raised."""
+    src = os.path.join(CSRC, "torch_marshal.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "pkv_ops.h")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return ""
+    torch_dir = spec.submodule_search_locations[0]
+    include = os.path.join(torch_dir, "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", INCLUDE, "-I", include, "-I",
+           os.path.join(include, "torch", "csrc", "api", "include"), "-I",
+           sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write("torch_marshal.cpp was not built (the Python marshalling serves):\n"
+                         + r.stderr[-2000:])
+        return ""
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "pkv_ops_internal.h"
@@ -99,6 +100,8 @@ pkv_status rope_append(pkv::RopeParams &p, int64_t num_blocks, bool fp8, void *s
     if (p.D > max_dim || p.Hkv > 1024 || p.Hq > 65536 || p.n > (int64_t(1) << 30) ||
         num_blocks > (int64_t(1) << 40) || !isfinite(p.scale))
         return PKV_ERR_RANGE;
+    if (fp8 && p.n > INT32_MAX / (1 + 2 * ((p.Hkv + 7) / 8)))
+        return PKV_ERR_RANGE;  // the grid
     const int64_t kv_row = int64_t(p.Hkv) * p.D, q_row = int64_t(p.Hq) * p.D;
     if (p.k_stride < kv_row || p.v_stride < kv_row || (p.Hq > 0 && p.q_stride < q_row))
         return PKV_ERR_SHAPE;
@@ -172,9 +175,17 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     DeviceLimits dev;
     if (device_limits(&dev) != cudaSuccess)
         return PKV_ERR_CUDA;
-    pkv::DecodePlan pl;
-    if (pkv::plan_scored(num_seqs, nq, Hq, Hkv, D, max_blocks_per_seq, dev.sms, dev.smem, fp8,
-                         &pl) != 0)
+    pkv::ScoredPlan pl;
+    // a window that reaches back over the longest possible context hides nothing; one that
+    // does not bounds the blocks a sequence reads
+    if (int64_t(window) >= int64_t(max_blocks_per_seq) * pkv::kBlockSize)
+        window = 0;
+    const int most_blocks =
+        window > 0 ? int(std::min<int64_t>(max_blocks_per_seq,
+                                           (int64_t(window) + nq + 2 * pkv::kBlockSize - 3) /
+                                               pkv::kBlockSize))
+                   : max_blocks_per_seq;
+    if (pkv::plan_scored(num_seqs, nq, Hq, Hkv, D, most_blocks, dev.sms, dev.smem, fp8, &pl) != 0)
         return PKV_ERR_UNSUPPORTED;
     if (workspace_bytes < pl.ws_bytes)
         return PKV_ERR_WORKSPACE;
@@ -216,8 +227,8 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     constexpr float kLog2e = 1.4426950408889634f;
     p.mul = softcap > 0.f ? 2.f * scale * kLog2e / softcap : scale * kLog2e;
     p.cap_log2 = softcap * kLog2e;
-    // a window that reaches back over the longest possible context hides nothing
-    p.window = int64_t(window) >= int64_t(max_blocks_per_seq) * pkv::kBlockSize ? 0 : window;
+    p.window = window;
+    p.whole = pl.whole;
     p.scale_vec = fp8 && pl.HG == 8 && aligned(k_scale, 8) && aligned(v_scale, 8);
     return pkv::launch_scored(pl, p, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
@@ -307,7 +318,7 @@ size_t pkv_workspace_size_scored(int32_t num_seqs, int32_t n_query_per_seq, int3
     // the larger of the two pool types; a plan's size does not grow with the table width
     size_t bytes = 0;
     for (int fp8 = 0; fp8 < 2; ++fp8) {
-        pkv::DecodePlan pl;
+        pkv::ScoredPlan pl;
         if ((fp8 && head_dim != 128) ||
             pkv::plan_scored(num_seqs, n_query_per_seq, num_q_heads, num_kv_heads, head_dim, 1,
                              dev.sms, dev.smem, fp8, &pl) != 0)

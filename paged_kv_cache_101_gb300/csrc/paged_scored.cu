@@ -122,21 +122,31 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     const DecodeParams &d = p.d;
     const int S = d.S;
     int64_t total = 0;
-    for (int s = lane; s < S; s += 32)
-        total += span(p, s).nb;
+    if (!p.whole) {
+#pragma unroll 8
+        for (int s = lane; s < S; s += 32)
+            total += span(p, s).nb;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        total += __shfl_xor_sync(kFull, total, o);
+        for (int o = 16; o >= 1; o >>= 1)
+            total += __shfl_xor_sync(kFull, total, o);
+    }
     Cells C;
     C.F = C.F1 = int64_t(d.n_hg) * total;
     C.F2 = 0;
     C.G = int(gridDim.x);
     C.NT = 0;
-    if (blockIdx.x == 0 && lane == 0) {
+    if (blockIdx.x == 0 && lane == 0 && !p.whole) {
         d.ws[kWsUnits] = uint32_t(total);
         d.ws[kWsDense] = C.F >= C.G ? 1u : 0u;
     }
-    const int64_t a = C.start(blockIdx.x), e = C.start(int64_t(blockIdx.x) + 1);
+    int64_t a, e;
+    if (p.whole) {
+        a = 0;
+        e = span(p, int(blockIdx.x) % S).nb;
+    } else {
+        a = C.start(blockIdx.x);
+        e = C.start(int64_t(blockIdx.x) + 1);
+    }
     Turn turn;
     uint32_t issued = 0;
     bool ok = true;
@@ -152,31 +162,34 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     };
 
     if (a < e) {
-        int hg = int(a / total);
-        int64_t rest = a - int64_t(hg) * total;
-        // the sequence that holds unit `rest` of its head group
-        int s = 0;
-        Span sp{0, 0, 0};
-        int b = 0;
-        for (int s0 = 0; s0 < S; s0 += 32) {
-            const int mine = s0 + lane < S ? span(p, s0 + lane).nb : 0;
-            int64_t incl = mine;
+        int hg, s = 0, b = 0;
+        if (p.whole) {
+            hg = int(blockIdx.x) / S;
+            s = int(blockIdx.x) - hg * S;
+        } else {
+            // the sequence that holds unit `rest` of its head group
+            hg = int(a / total);
+            int64_t rest = a - int64_t(hg) * total;
+            for (int s0 = 0; s0 < S; s0 += 32) {
+                const int mine = s0 + lane < S ? span(p, s0 + lane).nb : 0;
+                int64_t incl = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(kFull, incl, o);
-                if (lane >= o)
-                    incl += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t v = __shfl_up_sync(kFull, incl, o);
+                    if (lane >= o)
+                        incl += v;
+                }
+                const unsigned past = __ballot_sync(kFull, incl > rest);
+                if (past) {
+                    const int src = __ffs(past) - 1;
+                    s = s0 + src;
+                    b = int(rest - __shfl_sync(kFull, incl - mine, src));
+                    break;
+                }
+                rest -= __shfl_sync(kFull, incl, 31);
             }
-            const unsigned past = __ballot_sync(kFull, incl > rest);
-            if (past) {
-                const int src = __ffs(past) - 1;
-                s = s0 + src;
-                b = int(rest - __shfl_sync(kFull, incl - mine, src));
-                break;
-            }
-            rest -= __shfl_sync(kFull, incl, 31);
         }
-        sp = span(p, s);
+        Span sp = span(p, s);
         b = sp.b0 + sp.nb - 1 - b;  // the newest block comes first
         const uint64_t policy = policy_evict_first();
         const bool vec = FP8 && p.scale_vec;
@@ -232,11 +245,13 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
             if (lane == 0) {
                 // the merge's record: cell (and slot) of the sequence's first piece,
                 // cell of its last
-                int2 *rec = d.pieces + int64_t(s) * d.n_hg + hg;
-                if (b == b_top)
-                    rec->x = int(blockIdx.x) * 2 + (opens ? 0 : 1);
-                if (ends)
-                    rec->y = int(blockIdx.x);
+                if (!p.whole) {
+                    int2 *rec = d.pieces + int64_t(s) * d.n_hg + hg;
+                    if (b == b_top)
+                        rec->x = int(blockIdx.x) * 2 + (opens ? 0 : 1);
+                    if (ends)
+                        rec->y = int(blockIdx.x);
+                }
                 const int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) |
                                   (ends && from_top ? F_DIRECT : 0);
                 int4 *h = reinterpret_cast<int4 *>(&ring.hdr[turn.st]);
@@ -301,6 +316,22 @@ __device__ __forceinline__ float rcp(float x)
 constexpr float kLead = 8.f;
 // E4M3: weights are scaled by 2^6 (at most 2^14 with the lead; f16 ends at 2^16)
 constexpr int kWeightBits = 6;
+
+// A whole-sequence CTA whose sequence has no token: zeros for its heads.
+template <int D>
+__device__ __forceinline__ void clear_empty(const ScoredParams &p, int tid, int threads)
+{
+    const DecodeParams &d = p.d;
+    const int hg = int(blockIdx.x) / d.S, s = int(blockIdx.x) - hg * d.S;
+    if (seq_tokens(d, s) > 0)
+        return;
+    const int row = d.HG * d.G * D / (d.out_f32 ? 4 : 8);  // 16-byte words
+    for (int e = tid; e < d.nq * row; e += threads) {
+        const int j = e / row;
+        static_cast<uint4 *>(d.out)[((int64_t(s) * d.nq + j) * d.n_hg + hg) * row + e - j * row] =
+            make_uint4(0, 0, 0, 0);
+    }
+}
 
 // The rows of a warp: NT n-tiles of 8, a lane holding rows 2 tq and 2 tq + 1 of each,
 // tokens g and g + 8 of each of up to BL blocks.
@@ -732,6 +763,8 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
 }
 
 constexpr int kConsumers = 8;
+// A CTA alone streams this much in about the time that the join of pieces takes.
+constexpr int64_t kWholeBytes = 256 * 1024;
 
 template <int D, bool FP8, int NT, int WPH>
 __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
@@ -755,14 +788,17 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
     __syncthreads();
     if (warp == p.d.ncw)
         producer<FP8>(&kmap, &vmap, p, ring, lane);
-    else
+    else {
+        if (p.whole)
+            clear_empty<D>(p, threadIdx.x, 32 * p.d.ncw);
         consumer<D, FP8, NT, WPH>(p, ring, warp, lane);
+    }
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 template <int D, bool FP8, int NT, int WPH>
-cudaError_t launch_one(const DecodePlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
+cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
                        const CUtensorMap &vmap, cudaStream_t stream)
 {
     const auto kern = scored_kernel<D, FP8, NT, WPH>;
@@ -783,15 +819,15 @@ cudaError_t launch_one(const DecodePlan &pl, const ScoredParams &p, const CUtens
     e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
     if (e != cudaSuccess)
         return e;
-    return launch_merge(pl, p.d, stream);
+    return pl.whole ? cudaGetLastError() : launch_merge(pl, p.d, stream);
 }
 
 }  // namespace
 
 int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
-                int fp8, DecodePlan *pl)
+                int fp8, ScoredPlan *pl)
 {
-    DecodePlan P{};
+    ScoredPlan P{};
     P.D = D;
     P.kv8 = fp8;
     P.G = Hq / Hkv;
@@ -820,6 +856,11 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     P.smem = 1024 + size_t(P.nst) * per_stage;
     const int cap = P.ctas_per_sm * num_sms;
     P.grid = int(std::min<int64_t>(cap, int64_t(P.n_hg) * S * MB));
+    // few and short sequences: one CTA each, no second launch to join pieces
+    if (int64_t(P.n_hg) * S <= cap && int64_t(MB) * P.stage_bytes <= kWholeBytes) {
+        P.whole = 1;
+        P.grid = P.n_hg * S;
+    }
     P.off_rec = kWsHeaderBytes;
     P.off_ml = P.off_rec + round_up(size_t(S) * P.n_hg * 8, 256);
     P.off_part = P.off_ml + round_up(size_t(cap) * 2 * P.HG * P.rows * 2 * 4, 256);
@@ -828,7 +869,7 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     return 0;
 }
 
-cudaError_t launch_scored(const DecodePlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
+cudaError_t launch_scored(const ScoredPlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
                           const CUtensorMap &vmap, cudaStream_t stream)
 {
     if (pl.kv8) {

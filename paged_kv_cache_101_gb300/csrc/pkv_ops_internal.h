@@ -44,14 +44,20 @@ struct ScoredParams {
     float mul;               // to the log2 domain: scale log2(e), or 2 scale log2(e) / softcap
     float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
+    int whole;               // 1: CTA c has sequence c % S of head group c / S to itself
     int scale_vec;           // the scale bytes of a block's heads are an aligned 8-byte word
 };
 
-// The plan of a scored call (fp8: block-scaled pools); 0, or -1 if unsupported.
-int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
-                int fp8, DecodePlan *plan);
+struct ScoredPlan : DecodePlan {
+    int whole;  // every CTA has a sequence of a head group to itself: no pieces, no merge
+};
 
-cudaError_t launch_scored(const DecodePlan &plan, const ScoredParams &p, const CUtensorMap &kmap,
+// The plan of a scored call (fp8: block-scaled pools), MB the most blocks that a
+// sequence reads; 0, or -1 if unsupported.
+int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
+                int fp8, ScoredPlan *plan);
+
+cudaError_t launch_scored(const ScoredPlan &plan, const ScoredParams &p, const CUtensorMap &kmap,
                           const CUtensorMap &vmap, cudaStream_t stream);
 
 }  // namespace pkv

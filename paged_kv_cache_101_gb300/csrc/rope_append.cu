@@ -23,7 +23,16 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr unsigned kAll = 0xffffffffU;
 constexpr int kMaxPairs = 512;  // head_dim <= 1024
+
+// Launched with programmatic serialization: wait for the kernel before this one on the
+// stream, then let the one behind it start its own prologue.
+__device__ __forceinline__ void begin_after_previous()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
 
 __device__ __forceinline__ float2 turn(int64_t position, uint64_t turns, float scale)
 {
@@ -60,30 +69,40 @@ __device__ __forceinline__ void unpack8(uint4 w, float *x)
     x[7] = bf16hi_f32(w.w);
 }
 
-// The 16 values of unit u of the head at `src`, plain (rows of v).
-template <int FORM>
-__device__ __forceinline__ void load_unit(const uint16_t *src, int d0, int d1, int D, float *x)
+// A unit as it lies in memory (zeros where it has only eight dims).
+struct Raw {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const uint16_t *src, int d0, int d1, int D)
 {
-    unpack8(*reinterpret_cast<const uint4 *>(src + d0), x);
-    if (d1 < D)
-        unpack8(*reinterpret_cast<const uint4 *>(src + d1), x + 8);
-    else
-#pragma unroll
-        for (int i = 8; i < 16; ++i)
-            x[i] = 0.f;
+    Raw w;
+    w.a = *reinterpret_cast<const uint4 *>(src + d0);
+    w.b = d1 < D ? *reinterpret_cast<const uint4 *>(src + d1) : make_uint4(0, 0, 0, 0);
+    return w;
 }
 
-// The same, rotated by the row's `trig` (cos, sin of each pair).
-template <int FORM>
-__device__ __forceinline__ void load_rotated(const uint16_t *src, int u, int d0, int d1,
-                                             const RopeParams &p, const float2 *trig, float *x)
+__device__ __forceinline__ void unpack16(const Raw &w, float *x)
 {
-    load_unit<FORM>(src, d0, d1, p.D, x);
+    unpack8(w.a, x);
+    unpack8(w.b, x + 8);
+}
+
+// Where pair j's cosine and sine stand: the units' c-th pairs side by side, so that the
+// lanes of a warp, each at another unit, read from different banks.
+__device__ __forceinline__ int trig_at(int j, int half) { return (j & 7) * ((half + 7) / 8) + j / 8; }
+
+// Rotate a unit's values by the row's `trig` (cos, sin of each pair); kScalar reads the
+// partners at `src`.
+template <int FORM>
+__device__ __forceinline__ void rotate_unit(const uint16_t *src, int u, int d0, const RopeParams &p,
+                                            const float2 *trig, float *x)
+{
     if (FORM == kHalf) {
         if (u < p.r / 16) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 t = trig[d0 + i];
+                const float2 t = trig[trig_at(8 * u + i, p.r / 2)];
                 const float a = x[i], b = x[i + 8];
                 x[i] = a * t.x - b * t.y;
                 x[i + 8] = b * t.x + a * t.y;
@@ -92,9 +111,8 @@ __device__ __forceinline__ void load_rotated(const uint16_t *src, int u, int d0,
     } else if (FORM == kPairs) {
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const int d = (i < 8 ? d0 : d1 - 8) + i;
-            if (d < p.r) {
-                const float2 t = trig[d / 2];
+            if (d0 + i < p.r) {  // the unit's dims follow one another
+                const float2 t = trig[trig_at((d0 + i) / 2, p.r / 2)];
                 const float a = x[i], b = x[i + 1];
                 x[i] = a * t.x - b * t.y;
                 x[i + 1] = b * t.x + a * t.y;
@@ -109,7 +127,7 @@ __device__ __forceinline__ void load_rotated(const uint16_t *src, int u, int d0,
                 const bool second = p.interleaved ? (d & 1) : d >= h;
                 const int j = p.interleaved ? d / 2 : (second ? d - h : d);
                 const int o = p.interleaved ? d ^ 1 : (second ? j : d + h);
-                const float2 t = trig[j];
+                const float2 t = trig[trig_at(j, h)];
                 const float other = __uint_as_float(uint32_t(src[o]) << 16);
                 x[i] = second ? x[i] * t.x + other * t.y : x[i] * t.x - other * t.y;
             }
@@ -138,25 +156,27 @@ __device__ __forceinline__ void rotate_q(const RopeParams &p, int64_t i, const f
         const int h = e / p.units, u = e - h * p.units;
         int d0, d1;
         unit_dims<FORM>(u, p.r, p.D, d0, d1);
+        const uint16_t *src = p.q + i * p.q_stride + h * p.D;
         float x[16];
-        load_rotated<FORM>(p.q + i * p.q_stride + h * p.D, u, d0, d1, p, trig, x);
+        unpack16(load_raw(src, d0, d1, p.D), x);
+        rotate_unit<FORM>(src, u, d0, p, trig, x);
         store_unit(p.q_out + (i * p.Hq + h) * p.D, d0, d1, p.D, x);
     }
 }
 
-// bf16 pools: one CTA per row.
+// Any rotary_dim and head_dim: one CTA per row, its sines and cosines in shared memory.
 template <int FORM>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p)
+__global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopeParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ float2 trig[kMaxPairs];
+    begin_after_previous();
+    __shared__ float2 trig[kMaxPairs + 8];
     const int64_t i = blockIdx.x;
     const int64_t pos = __ldg(p.positions + i);
     for (int j = threadIdx.x; j < p.r / 2; j += kThreads)
-        trig[j] = turn(pos, __ldg(p.turns + j), p.scale);
+        trig[trig_at(j, p.r / 2)] = turn(pos, __ldg(p.turns + j), p.scale);
     __syncthreads();
     rotate_q<FORM>(p, i, trig);
-    const int64_t slot = __ldg(p.slots + i);
+    const int64_t slot = p.k_scale ? -1 : __ldg(p.slots + i);
     if (slot < 0 || slot >= p.total_slots)
         return;
     for (int e = threadIdx.x; e < 2 * p.Hkv * p.units; e += kThreads) {
@@ -166,15 +186,123 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
         h -= is_v ? p.Hkv : 0;
         int d0, d1;
         unit_dims<FORM>(u, p.r, p.D, d0, d1);
+        const uint16_t *src = is_v ? p.v + i * p.v_stride + h * p.D : p.k + i * p.k_stride + h * p.D;
         float x[16];
-        if (is_v)
-            load_unit<FORM>(p.v + i * p.v_stride + h * p.D, d0, d1, p.D, x);
-        else
-            load_rotated<FORM>(p.k + i * p.k_stride + h * p.D, u, d0, d1, p, trig, x);
+        unpack16(load_raw(src, d0, d1, p.D), x);
+        if (!is_v)
+            rotate_unit<FORM>(src, u, d0, p, trig, x);
         store_unit(static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) +
                        (slot * p.Hkv + h) * p.D,
                    d0, d1, p.D, x);
     }
+}
+
+// Vector forms with at most 32 units a head: `split` warps of a CTA share a row, each
+// taking every split-th group of heads. A lane keeps one unit of its head, so its
+// eight sines and cosines stay in registers for all heads of the row; no shared
+// memory, no barrier, kAhead heads' loads in flight a lane. KV: k and v as well (the
+// block-scaled append runs this for q alone).
+template <int FORM, bool KV>
+__device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int part, int split,
+                                           int lane)
+{
+    constexpr int kAhead = 3;
+    const int per = 32 / p.units;  // heads of one group
+    const int u = lane % p.units, sub = lane / p.units;
+    int d0, d1;
+    unit_dims<FORM>(u, p.r, p.D, d0, d1);
+    const bool two = d1 < p.D;
+    const int64_t slot = KV ? __ldg(p.slots + i) : -1;
+    const bool stored = slot >= 0 && slot < p.total_slots;
+    const int64_t pos = __ldg(p.positions + i);
+    float2 t[8];
+    // pair 8 u + c is the unit's c-th in both layouts
+    const bool turns = FORM == kHalf ? u < p.r / 16 : 16 * u < p.r;
+    auto pair = [&](int c) {
+        return turns && 8 * u + c < p.r / 2 ? turn(pos, __ldg(p.turns + 8 * u + c), p.scale)
+                                            : make_float2(0.f, 0.f);
+    };
+    if (per == 4) {
+        // four lanes hold the same unit of four heads: each computes two pairs for all
+        const float2 lo = pair(sub), hi = pair(sub + 4);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float2 from = c < 4 ? lo : hi;
+            t[c].x = __shfl_sync(kAll, from.x, (c & 3) * p.units + u);
+            t[c].y = __shfl_sync(kAll, from.y, (c & 3) * p.units + u);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            t[c] = pair(c);
+    }
+    // groups of q heads, then of k's and v's (of one kind each: the choice is the warp's)
+    const int nq = (p.Hq + per - 1) / per, nk = KV ? (p.Hkv + per - 1) / per : 0;
+    const int groups = nq + (stored ? 2 * nk : 0);
+    for (int g0 = part; g0 < groups; g0 += split * kAhead) {
+        uint4 a[kAhead], b[kAhead];
+        uint16_t *to[kAhead];
+        bool rot[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            int group = g0 + k * split, heads = p.Hq;
+            const uint16_t *from = p.q + i * p.q_stride;
+            uint16_t *dst = p.q_out + i * p.Hq * p.D;
+            const bool in = group < groups;
+            rot[k] = turns;
+            if (KV && group >= nq) {
+                group -= nq;
+                heads = p.Hkv;
+                const bool is_v = group >= nk;
+                group -= is_v ? nk : 0;
+                from = is_v ? p.v + i * p.v_stride : p.k + i * p.k_stride;
+                dst = static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + slot * p.Hkv * p.D;
+                rot[k] = turns && !is_v;
+            }
+            const int h = group * per + sub;
+            to[k] = in && sub < per && h < heads ? dst + h * p.D : nullptr;
+            a[k] = b[k] = make_uint4(0, 0, 0, 0);
+            if (to[k]) {
+                a[k] = *reinterpret_cast<const uint4 *>(from + h * p.D + d0);
+                if (two)
+                    b[k] = *reinterpret_cast<const uint4 *>(from + h * p.D + d1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (!to[k])
+                continue;
+            if (rot[k]) {
+                float x[16];
+                unpack8(a[k], x);
+                unpack8(b[k], x + 8);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int m = FORM == kHalf ? c : 2 * c, n = FORM == kHalf ? c + 8 : 2 * c + 1;
+                    if (FORM == kHalf || 8 * u + c < p.r / 2) {
+                        const float v = x[m], w = x[n];
+                        x[m] = v * t[c].x - w * t[c].y;
+                        x[n] = w * t[c].x + v * t[c].y;
+                    }
+                }
+                a[k] = pack8(x);
+                b[k] = pack8(x + 8);
+            }
+            *reinterpret_cast<uint4 *>(to[k] + d0) = a[k];
+            if (two)
+                *reinterpret_cast<uint4 *>(to[k] + d1) = b[k];
+        }
+    }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const RopeParams p, int split)
+{
+    begin_after_previous();
+    const int warp = threadIdx.x >> 5, rows = kThreads / 32 / split;
+    const int64_t i = int64_t(blockIdx.x) * rows + warp / split;
+    if (i < p.n)
+        rotate_row<FORM, true>(p, i, warp % split, split, threadIdx.x & 31);
 }
 
 __device__ __forceinline__ uint2 encode8(const float *x, float f)
@@ -211,102 +339,126 @@ __device__ __forceinline__ uint2 rescale8(uint2 w, float f)
     return encode8(x, f);
 }
 
-// Block-scaled E4M3 pools. CTAs [0, n) rotate q; CTA n + i serves the block that row
-// i opens in the batch (row i - 1 falls elsewhere): the run of up to 16 rows that
-// fall into it, one warp for each (kv head, K or V). The warp finds the run's
-// largest magnitude, settles the block's scale, rounds the block's earlier codes
-// to it if it grew, and writes the run.
-template <int FORM>
-__global__ void __launch_bounds__(kThreads) rope_append_fp8_kernel(const RopeParams p)
+// Round a block's codes of one head to a larger scale (one warp; `vecs` 8-byte words a
+// row). Not inlined: it happens a few times in a block's life, and its registers would
+// be the run's.
+__device__ __noinline__ void rescale_block(uint8_t *codes, int64_t row_bytes, int vecs, float f,
+                                           int lane)
 {
-    asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ float2 trig[kBlockSize * kMaxFp8BlockDim / 2];
-    const int tid = threadIdx.x, half = p.r / 2;
-    if (blockIdx.x < p.n && p.Hq > 0) {
-        const int64_t i = blockIdx.x;
-        const int64_t pos = __ldg(p.positions + i);
-        for (int j = tid; j < half; j += kThreads)
-            trig[j] = turn(pos, __ldg(p.turns + j), p.scale);
-        __syncthreads();
-        rotate_q<FORM>(p, i, trig);
-        return;
-    }
-    const int64_t i0 = blockIdx.x - (p.Hq > 0 ? p.n : 0);
-    auto block_of = [&](int64_t i) -> int64_t {
-        const int64_t s = __ldg(p.slots + i);
-        return s < 0 || s >= p.total_slots ? -1 : s / kBlockSize;
-    };
-    const int64_t block = block_of(i0);
-    if (block < 0 || (i0 > 0 && block_of(i0 - 1) == block))
-        return;
-    int rows = 1;
-    bool begun = __ldg(p.slots + i0) % kBlockSize == 0;
-    while (rows < kBlockSize && i0 + rows < p.n && block_of(i0 + rows) == block) {
-        begun |= __ldg(p.slots + i0 + rows) % kBlockSize == 0;
-        ++rows;
-    }
-    for (int e = tid; e < rows * half; e += kThreads) {
-        const int rr = e / half, j = e - rr * half;
-        trig[e] = turn(__ldg(p.positions + i0 + rr), __ldg(p.turns + j), p.scale);
-    }
-    __syncthreads();
-
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int task = warp; task < 2 * p.Hkv; task += kThreads / 32) {
-        const bool is_v = task >= p.Hkv;
-        const int h = is_v ? task - p.Hkv : task;
-        uint8_t *codes = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) +
-                         (block * kBlockSize * p.Hkv + h) * p.D;
-        uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + block * p.Hkv + h;
-        auto value = [&](int rr, int u, int d0, int d1, float *x) {
-            const int64_t i = i0 + rr;
-            if (is_v)
-                load_unit<FORM>(p.v + i * p.v_stride + h * p.D, d0, d1, p.D, x);
-            else
-                load_rotated<FORM>(p.k + i * p.k_stride + h * p.D, u, d0, d1, p, trig + rr * half, x);
-        };
-        float amax = 0.f;
-        for (int e = lane; e < rows * p.units; e += 32) {
-            const int rr = e / p.units, u = e - rr * p.units;
-            int d0, d1;
-            unit_dims<FORM>(u, p.r, p.D, d0, d1);
-            float x[16];
-            value(rr, u, d0, d1, x);
+    for (int e0 = 0; e0 < kBlockSize * vecs; e0 += 8 * 32) {
+        uint2 w[8], *to[8];  // eight loads wait together
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float a = fabsf(x[c]);
-                amax = fmaxf(amax, a <= FLT_MAX ? a : 0.f);
+        for (int k = 0; k < 8; ++k) {
+            const int e = e0 + 32 * k + lane, rr = e / vecs, c = e - rr * vecs;
+            to[k] = reinterpret_cast<uint2 *>(codes + rr * row_bytes + 8 * c);
+            if (rr < kBlockSize)
+                w[k] = *to[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if ((e0 + 32 * k + lane) / vecs < kBlockSize)
+                *to[k] = rescale8(w[k], f);
+    }
+}
+
+// The scale byte of a block and head (`old`, 0: started here) once rows of largest finite
+// magnitude amax join it: written where it changed, the codes so far rounded to it.
+__device__ __forceinline__ int settle(float amax, int old, uint8_t *codes, uint8_t *scale,
+                                      int64_t row_bytes, int vecs, int lane)
+{
+    // the smallest byte with amax <= 448 * 2^(byte - 127): 448 = 1.75 * 2^8
+    const uint32_t bits = __float_as_uint(amax);
+    int code = int(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    code = code < 1 ? 1 : code;
+    code = old > code ? old : code;
+    __syncwarp();  // every lane has read the old byte
+    if (lane == 0 && code != old)
+        *scale = uint8_t(code);
+    if (old > 0 && code > old) {
+        rescale_block(codes, row_bytes, vecs, two_to(old - code), lane);
+        __syncwarp();  // the new rows come after
+    }
+    return code;
+}
+
+// Where pass after pass of a warp over a run's units stands: unit u of row rr.
+struct UnitAt {
+    int rr, u, step_r, step_u, units;
+    __device__ __forceinline__ UnitAt(int lane, int units_)
+        : rr(lane / units_), u(lane - lane / units_ * units_), step_r(32 / units_),
+          step_u(32 - 32 / units_ * units_), units(units_)
+    {
+    }
+    __device__ __forceinline__ void next()
+    {
+        rr += step_r;
+        u += step_u;
+        if (u >= units) {
+            u -= units;
+            ++rr;
+        }
+    }
+};
+
+// One run: up to 16 rows from i0 that fall into one block, for head h of K or V, by one
+// warp. It holds the run in registers, finds its largest magnitude, settles the block's
+// scale, rounds the block's earlier codes to it if it grew, and writes the run. Lane
+// l0 + r brings the slot of row i0 + r; `raw` the run's rows, pass by pass; trig its
+// sines and cosines; `old` the block's scale byte (0: the run starts the block).
+template <int FORM, int PASSES>
+__device__ __forceinline__ void append_run(const RopeParams &p, const Raw (&raw)[PASSES], int64_t i0,
+                                           int rows, int64_t block, int old, int64_t slot,
+                                           int l0, bool is_v, int h, const float2 *trig,
+                                           const UnitAt &start, int lane)
+{
+    const int pitch = (p.r / 2 + 7) / 8 * 8;
+    uint8_t *codes = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) +
+                     (block * kBlockSize * p.Hkv + h) * p.D;
+    uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + block * p.Hkv + h;
+    // pass k: unit e % units of row e / units of the run, e = lane + 32 k. The values are
+    // computed twice, for the largest magnitude and for the codes: kept, they would take
+    // 64 registers and with them half of the CTAs of an SM.
+    auto values = [&](int k, int rr, int u, int d0, float *x) {
+        unpack16(raw[k], x);
+        if (!is_v)
+            rotate_unit<FORM>(p.k + (i0 + rr) * p.k_stride + h * p.D, u, d0, p, trig + rr * pitch, x);
+    };
+    auto largest = [&](float below) {
+        float amax = 0.f;
+        UnitAt at = start;
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k, at.next()) {
+            if (at.rr < rows) {
+                int d0, d1;
+                unit_dims<FORM>(at.u, p.r, p.D, d0, d1);
+                float x[16];
+                values(k, at.rr, at.u, d0, x);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)  // (fmaxf passes over NaN)
+                    amax = fmaxf(amax, below == INFINITY || fabsf(x[c]) <= below ? fabsf(x[c]) : 0.f);
             }
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // the smallest byte with amax <= 448 * 2^(byte - 127): 448 = 1.75 * 2^8
-        const uint32_t bits = __float_as_uint(amax);
-        int code = int(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        code = code < 1 ? 1 : code;
-        const int old = begun ? 0 : *scale;
-        code = old > code ? old : code;
-        __syncwarp();  // every lane has read the scale
-        if (lane == 0)
-            *scale = uint8_t(code);
-        if (old > 0 && code > old) {
-            const float f = two_to(old - code);
-            for (int e = lane; e < kBlockSize * (p.D / 8); e += 32) {
-                const int rr = e / (p.D / 8), c = e - rr * (p.D / 8);
-                uint2 *w = reinterpret_cast<uint2 *>(codes + int64_t(rr) * p.Hkv * p.D + 8 * c);
-                *w = rescale8(*w, f);
-            }
-            __syncwarp();  // the new rows come after
-        }
-        const float inv = two_to(127 - code);
-        for (int e = lane; e < rows * p.units; e += 32) {
-            const int rr = e / p.units, u = e - rr * p.units;
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        return amax;
+    };
+    float amax = largest(INFINITY);
+    if (__builtin_expect(amax == INFINITY, 0))
+        amax = largest(FLT_MAX);  // an infinity among them: the largest finite one counts
+    const int code = settle(amax, old, codes, scale, p.Hkv * p.D, p.D / 8, lane);
+    const float inv = two_to(127 - code);
+    const int offset = int(slot) & (kBlockSize - 1);  // slots in use are not negative
+    UnitAt at = start;
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k, at.next()) {
+        const int to = __shfl_sync(kAll, offset, l0 + (at.rr < rows ? at.rr : 0));
+        if (at.rr < rows) {
             int d0, d1;
-            unit_dims<FORM>(u, p.r, p.D, d0, d1);
+            unit_dims<FORM>(at.u, p.r, p.D, d0, d1);
             float x[16];
-            value(rr, u, d0, d1, x);
-            uint8_t *row = codes + (__ldg(p.slots + i0 + rr) % kBlockSize) * p.Hkv * p.D;
+            values(k, at.rr, at.u, d0, x);
+            uint8_t *row = codes + to * p.Hkv * p.D;
             *reinterpret_cast<uint2 *>(row + d0) = encode8(x, inv);
             if (d1 < p.D)
                 *reinterpret_cast<uint2 *>(row + d1) = encode8(x + 8, inv);
@@ -314,16 +466,235 @@ __global__ void __launch_bounds__(kThreads) rope_append_fp8_kernel(const RopePar
     }
 }
 
+// The same for heads of 128 dims in vector form, eight units a row: lane l has unit l % 8
+// of rows l / 8, l / 8 + 4, ..
+template <int FORM>
+__device__ __forceinline__ void append_run_128(const RopeParams &p, const Raw (&raw)[4], int rows,
+                                               int64_t block, int old, int64_t slot, int l0,
+                                               bool is_v, int h, const float2 *trig, int pitch,
+                                               int lane)
+{
+    const int u = lane & 7, sub = lane >> 3;
+    const int64_t row_bytes = int64_t(p.Hkv) * 128;
+    uint8_t *codes = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) +
+                     block * kBlockSize * row_bytes + h * 128;
+    const int nu = pitch / 8;
+    const int pairs = is_v ? 0 : FORM == kHalf ? (u < p.r / 16 ? 8 : 0)
+                                               : min(max(p.r / 2 - 8 * u, 0), 8);
+    auto values = [&](int k, float *x) {
+        unpack16(raw[k], x);
+        const float2 *t = trig + (4 * k + sub) * pitch + u;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int m = FORM == kHalf ? c : 2 * c, n = FORM == kHalf ? c + 8 : 2 * c + 1;
+            if (c < pairs) {
+                const float2 cs = t[c * nu];
+                const float v = x[m], w = x[n];
+                x[m] = v * cs.x - w * cs.y;
+                x[n] = w * cs.x + v * cs.y;
+            }
+        }
+    };
+    auto largest = [&](float below) {
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (4 * k + sub < rows) {
+                float x[16];
+                values(k, x);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)  // (fmaxf passes over NaN)
+                    amax = fmaxf(amax, below == INFINITY || fabsf(x[c]) <= below ? fabsf(x[c]) : 0.f);
+            }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        return amax;
+    };
+    float amax = largest(INFINITY);
+    if (__builtin_expect(amax == INFINITY, 0))
+        amax = largest(FLT_MAX);  // an infinity among them: the largest finite one counts
+    const int code = settle(amax, old, codes, (is_v ? p.v_scale : p.k_scale) + block * p.Hkv + h,
+                            row_bytes, 16, lane);
+    const float inv = two_to(127 - code);
+    const int offset = int(slot) & (kBlockSize - 1);  // slots in use are not negative
+    int d0, d1;
+    unit_dims<FORM>(u, p.r, 128, d0, d1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int to = __shfl_sync(kAll, offset, (l0 + 4 * k + sub) & 31);
+        if (4 * k + sub < rows) {
+            float x[16];
+            values(k, x);
+            uint8_t *row = codes + to * row_bytes;
+            *reinterpret_cast<uint2 *>(row + d0) = encode8(x, inv);
+            *reinterpret_cast<uint2 *>(row + d1) = encode8(x + 8, inv);
+        }
+    }
+}
+
+// Block-scaled E4M3 pools. `q_ctas` CTAs rotate q. Of the others, CTA (w, y) serves the
+// runs that start in the `window` rows from w * window on (a row starts one where the
+// row before it falls into another block), for eight heads of K (y even) or V, a warp
+// each: windows of one row while the rows are few (every token of a decode step is a
+// run of its own), of eight and sixteen above (a prompt has a run in 16 rows, and a CTA
+// that finds none still costs its slot on an SM: 8,190 rows, K and V alone, 42.3 us with
+// eight rows looked at one after another, 24.9 us with one look at eight, 18.8 us at sixteen). Bound
+// by the latency of slots, then rows, then stores while rows are few (64 rows with q:
+// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 61.0 us, 77% of the measured copy
+// bandwidth: 46 us of it are q.
+// PASSES 0: heads of 128 dims in vector form.
+template <int FORM, int PASSES>
+__global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8_kernel(const RopeParams p, int split,
+                                                                   int64_t q_ctas, int window)
+{
+    begin_after_previous();
+    __shared__ float2 trig[kBlockSize * (kMaxFp8BlockDim / 2 + 8)];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = p.r / 2;
+    // the two kinds of CTAs are spread evenly over the grid, so that those that wait on
+    // latency run beside those that wait on bandwidth
+    const int64_t q_before = int64_t(blockIdx.x) * q_ctas / gridDim.x;
+    if ((int64_t(blockIdx.x) + 1) * q_ctas / gridDim.x > q_before) {
+        if constexpr (FORM != kScalar) {
+            const int64_t i = q_before * (kThreads / 32 / split) + warp / split;
+            if (i < p.n)
+                rotate_row<FORM, false>(p, i, warp % split, split, lane);
+        } else {
+            const int64_t i = q_before;
+            const int64_t pos = __ldg(p.positions + i);
+            for (int j = tid; j < half; j += kThreads)
+                trig[trig_at(j, half)] = turn(pos, __ldg(p.turns + j), p.scale);
+            __syncthreads();
+            rotate_q<FORM>(p, i, trig);
+        }
+        return;
+    }
+    const int groups = (p.Hkv + 7) / 8;
+    const int64_t at = blockIdx.x - q_before;
+    const int64_t w = at / (2 * groups);
+    const int y = int(at - w * (2 * groups));
+    const bool is_v = y & 1;
+    const int h = (y >> 1) * 8 + warp;
+    const uint64_t turns0 = __ldg(p.turns + tid % half);
+    const int pitch = (half + 7) / 8 * 8;
+    const UnitAt start(lane, p.units);
+    // lane l: slot and position of row w * window + l - 1 (the row before the window, the
+    // window, and the rows that its last run may reach)
+    const int64_t first = w * window - 1;
+    const bool in = first + lane >= 0 && first + lane < p.n && lane <= window + kBlockSize - 1;
+    const int64_t slot = in ? __ldg(p.slots + first + lane) : -1;
+    const int64_t pos = in && !is_v ? __ldg(p.positions + first + lane) : 0;
+    const int64_t mine = slot < 0 || slot >= p.total_slots ? -1 : slot / kBlockSize;
+    const int64_t before = __shfl_up_sync(kAll, mine, 1);
+    const unsigned opens = __ballot_sync(kAll, lane >= 1 && lane <= window && mine >= 0 &&
+                                                          mine != before);
+    for (unsigned left = opens; left != 0; left &= left - 1) {
+        const int l0 = __ffs(left) - 1;  // the run's first row is lane l0's
+        const int64_t i0 = first + l0;
+        const int64_t block = __shfl_sync(kAll, mine, l0);
+        const unsigned same = __ballot_sync(kAll, mine == block) >> l0;
+        const int rows = min(same == kAll ? 32 : __ffs(~same) - 1, kBlockSize);
+        const bool begun = __ballot_sync(kAll, lane >= l0 && lane < l0 + rows &&
+                                                          slot % kBlockSize == 0) != 0;
+        // the run's rows and scale are on their way while the sines are computed
+        Raw raw[PASSES ? PASSES : 4];
+        int old = 0;
+        if (h < p.Hkv) {
+            if (!begun)
+                old = (is_v ? p.v_scale : p.k_scale)[block * p.Hkv + h];
+            const int64_t stride = is_v ? p.v_stride : p.k_stride;
+            const uint16_t *src = (is_v ? p.v : p.k) + i0 * stride + h * p.D;
+            if constexpr (PASSES == 0) {
+                int d0, d1;
+                unit_dims<FORM>(lane & 7, p.r, 128, d0, d1);
+                src += (lane >> 3) * stride;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    raw[k].a = raw[k].b = make_uint4(0, 0, 0, 0);
+                    if (4 * k + (lane >> 3) < rows)
+                        raw[k] = load_raw(src + 4 * k * stride, d0, d1, 128);
+                }
+            }
+            UnitAt at = start;
+#pragma unroll
+            for (int k = 0; k < PASSES; ++k, at.next())
+                if (at.rr < rows) {
+                    int d0, d1;
+                    unit_dims<FORM>(at.u, p.r, p.D, d0, d1);
+                    raw[k] = load_raw(src + at.rr * stride, d0, d1, p.D);
+                }
+        }
+        if (!is_v) {
+            __syncthreads();  // the run before is written
+            for (int e0 = 0; e0 < rows * half; e0 += kThreads) {
+                const int e = e0 + tid, rr = e / half, j = e - rr * half;
+                const int64_t at_row = __shfl_sync(kAll, pos, l0 + (rr < rows ? rr : 0));
+                if (rr < rows)
+                    trig[rr * pitch + trig_at(j, half)] =
+                        turn(at_row, e0 == 0 ? turns0 : __ldg(p.turns + j), p.scale);
+            }
+            __syncthreads();
+        }
+        if (h >= p.Hkv)
+            continue;
+        if constexpr (PASSES == 0)
+            append_run_128<FORM>(p, raw, rows, block, old, slot, l0, is_v, h, trig, pitch, lane);
+        else
+            append_run<FORM, PASSES>(p, raw, i0, rows, block, old, slot, l0, is_v, h, trig, start,
+                                     lane);
+    }
+}
+
+// A launch whose start may overlap the end of the kernel before it on the stream (the
+// kernels wait before they touch memory).
+template <typename... K, typename... A>
+cudaError_t launch_overlapped(void (*kern)(K...), int64_t grid, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int FORM>
 cudaError_t launch(const RopeParams &p, cudaStream_t stream)
 {
+    constexpr int kWarps = kThreads / 32;
+    // warps of a row: all of a CTA's while the rows are few (latency); once they fill the
+    // GPU two, and one beside the block-scaled append, whose own arithmetic fills the issue
+    // slots (each warp of a row computes its sines and cosines again). 8,190 rows, 1 / 2 / 4
+    // warps: 34.9 / 33.8 / 36.9 us in bf16 (88% of the measured copy bandwidth), 65.7 /
+    // 69.6 / 78.5 us block-scaled (an earlier form of it).
+    const int split = p.n < 1024 ? kWarps : p.k_scale ? 1 : 2;
+    const int rows = kWarps / split;
+    const int64_t row_ctas = (p.n + rows - 1) / rows;
     if (p.k_scale) {
-        const int64_t grid = p.Hq > 0 ? 2 * p.n : p.n;
-        rope_append_fp8_kernel<FORM><<<unsigned(grid), kThreads, 0, stream>>>(p);
-    } else {
-        rope_append_kernel<FORM><<<unsigned(p.n), kThreads, 0, stream>>>(p);
+        const int64_t q_ctas = p.Hq == 0 ? 0 : FORM == kScalar ? p.n : row_ctas;
+        const int window = p.n < 1024 ? 1 : p.n < 4096 ? 8 : 16;
+        const int64_t grid = q_ctas + (p.n + window - 1) / window * 2 * ((p.Hkv + 7) / 8);
+        if constexpr (FORM != kScalar) {
+            if (p.D == 128)
+                return launch_overlapped(rope_append_fp8_kernel<FORM, 0>, grid, stream, p, split,
+                                         q_ctas, window);
+        }
+        if (p.units * kBlockSize <= 32 * 4)
+            return launch_overlapped(rope_append_fp8_kernel<FORM, 4>, grid, stream, p, split,
+                                     q_ctas, window);
+        return launch_overlapped(rope_append_fp8_kernel<FORM, 8>, grid, stream, p, split, q_ctas,
+                                 window);
     }
-    return cudaGetLastError();
+    if constexpr (FORM != kScalar) {
+        if (p.units <= 32)
+            return launch_overlapped(rope_append_kernel<FORM>, row_ctas, stream, p, split);
+    }
+    return launch_overlapped(rope_append_any_kernel<FORM>, p.n, stream, p);
 }
 
 }  // namespace

@@ -1,7 +1,9 @@
 """Operators beside the decode path (``include/pkv_ops.h``): rotary positions on the
 way into the cache, block-scaled E4M3 pools, and attention with capped scores, a
 distance bias or a sliding window. Argument marshalling only, as the package's
-other functions.
+other functions: a call that is in order goes through ``csrc/torch_marshal.cpp`` (about
+1 us), anything else through the checks below, which say what is wrong (and make the
+call themselves where the marshaller was not built).
 
     turns = rotary_turns(rotary_dim, base)                  # once, host
     rope_kv_append(q, k_new, v_new, positions, turns, slot_mapping, k_cache, v_cache, q_out)
@@ -23,6 +25,33 @@ import ctypes
 import functools
 
 import paged_kv_cache_101_gb300 as _pkv
+
+_fast = None      # the C++ marshaller (csrc/torch_marshal.cpp), or False without it
+_torch = None
+
+
+def _load():
+    """Load the marshaller and hand it the library's entry points."""
+    global _fast, _torch
+    _torch = _pkv._torch()
+    lib = _pkv.lib()
+    try:
+        from . import _torch_marshal as fast
+    except ImportError:
+        _fast = False
+        return _fast
+    fast.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "pkv_rope_kv_append", "pkv_rope_kv_append_fp8_block", "pkv_paged_decode_attention_scored",
+        "pkv_workspace_size_scored")))
+    _fast = fast
+    return _fast
+
+
+def _here():
+    """The current device and its current stream's handle."""
+    dev = _torch._C._cuda_getDevice()
+    return dev, _torch._C._cuda_getCurrentRawStream(dev)
+
 
 _KINDS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 
@@ -131,6 +160,14 @@ def rope_kv_append(q, k_new, v_new, positions, turns, slot_mapping, k_cache, v_c
     ``turns``: ``rotary_turns(...)`` on the device, half as long as the rotated part of
     a head. q, k_new and v_new may be slices of one ``[n, ...]`` projection output;
     ``q`` and ``q_out`` None: keys and values only."""
+    if _fast or _fast is None and _load():
+        try:
+            st = _fast.rope(q, k_new, v_new, positions, turns, slot_mapping, k_cache, v_cache,
+                            None, None, q_out, interleaved, rotary_scale, *_here())
+        except RuntimeError:  # no device
+            st = None
+        if st == _pkv.PKV_OK:
+            return q_out
     return _rope("pkv_rope_kv_append", q, k_new, v_new, positions, turns, slot_mapping, k_cache,
                  v_cache, (), q_out, interleaved, rotary_scale)
 
@@ -139,6 +176,15 @@ def rope_kv_append_fp8_block(q, k_new, v_new, positions, turns, slot_mapping, k_
                              k_scale, v_scale, q_out, interleaved=False, rotary_scale=1.0):
     """``rope_kv_append`` into block-scaled E4M3 pools; updates ``k_scale``, ``v_scale``
     (uint8 ``[num_blocks, Hkv]``). The rows of one block follow one another."""
+    if _fast or _fast is None and _load():
+        try:
+            st = None if k_scale is None else _fast.rope(
+                q, k_new, v_new, positions, turns, slot_mapping, k_cache, v_cache, k_scale,
+                v_scale, q_out, interleaved, rotary_scale, *_here())
+        except RuntimeError:
+            st = None
+        if st == _pkv.PKV_OK:
+            return q_out
     return _rope("pkv_rope_kv_append_fp8_block", q, k_new, v_new, positions, turns, slot_mapping,
                  k_cache, v_cache, (k_scale, v_scale), q_out, interleaved, rotary_scale)
 
@@ -173,6 +219,20 @@ def _workspace(dev, stream, nbytes):
 
 def _attend(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, n_query_per_seq,
             scale, out, softcap, alibi_slopes, window, ws):
+    if _fast or _fast is None and _load():
+        try:
+            dev, stream = _here()
+            if ws is None and not _torch.cuda.is_current_stream_capturing():
+                use = _workspaces.get((dev, stream))
+            else:
+                use = ws
+            st = _fast.attend(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                              n_query_per_seq, scale, out, softcap, alibi_slopes, window, use, dev,
+                              stream)
+        except RuntimeError:  # no device
+            st = None
+        if st == _pkv.PKV_OK:
+            return out
     torch = _pkv._torch()
     check = _pkv._check
     check(q, "q", torch.bfloat16, 3)

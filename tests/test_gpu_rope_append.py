@@ -78,7 +78,8 @@ def run(c, interleaved, scale=1.0):
     (1, 32, 8, 128, 128), (1, 1, 1, 8, 2), (5, 8, 2, 64, 64), (33, 7, 7, 80, 80),
     (19, 6, 3, 96, 24), (64, 64, 8, 128, 64), (17, 5, 5, 72, 40), (3, 2, 1, 256, 256),
     (2, 4, 2, 1024, 1024), (9, 4, 2, 24, 6), (11, 3, 1, 80, 20), (1000, 16, 2, 64, 32),
-    (6, 9, 3, 136, 112)])
+    (6, 9, 3, 136, 112), (1500, 4, 2, 128, 128), (1025, 3, 1, 80, 64), (2, 3, 1, 512, 512),
+    (4, 2, 1, 520, 64)])
 def test_rotation_and_append(n, Hq, Hkv, D, r, interleaved):
     run(Case(n, Hq, Hkv, D, r, pad=(0, n // 2) if n > 4 else ()), interleaved)
 

@@ -73,7 +73,8 @@ def rows(rng, n, H, D, spread=0.0):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("n,Hq,Hkv,D,r", [
     (1, 32, 8, 128, 128), (16, 4, 2, 128, 64), (17, 5, 5, 80, 80), (50, 3, 3, 72, 20),
-    (7, 2, 1, 256, 256), (100, 8, 4, 128, 128), (33, 2, 2, 64, 16)])
+    (7, 2, 1, 256, 256), (100, 8, 4, 128, 128), (33, 2, 2, 64, 16), (20, 3, 9, 128, 96),
+    (1500, 4, 2, 128, 64), (4500, 2, 1, 128, 128), (1200, 2, 1, 64, 64)])
 def test_one_run(n, Hq, Hkv, D, r, interleaved):
     """One sequence's chunk from position 5 on: a block continued, blocks started."""
     rng = np.random.default_rng(n + D + r)
@@ -103,6 +104,25 @@ def test_token_by_token():
         pool.append(R.bf16(rng.standard_normal((S, Hkv, D)) * size),
                     R.bf16(rng.standard_normal((S, Hkv, D)) * size), pos, turns, slots)
         pos = pos + (slots >= 0)
+
+
+@pytest.mark.parametrize("n,new", [(1100, 1), (1300, 3), (4200, 2)])
+def test_large_batches_of_short_runs(n, new):
+    """Many sequences with one to three tokens each: several runs in a CTA's window."""
+    rng = np.random.default_rng(n)
+    seqs = n // new
+    pool = Pools(2 * seqs + 3, 2, 128, seed=n, empty=False)
+    start = rng.integers(0, 20, seqs)
+    order = rng.permutation(2 * seqs).reshape(seqs, 2)
+    pos = (start[:, None] + np.arange(new)).reshape(-1)
+    at = (start[:, None] + np.arange(new)) % 32
+    slots = (np.take_along_axis(order, at // 16, 1) * 16 + at % 16).reshape(-1)
+    slots[rng.integers(0, slots.size, 40)] = -1
+    # a padding row inside a run would part its block's rows: pad whole sequences
+    bad = (slots.reshape(seqs, new) < 0).any(axis=1)
+    slots = np.where(np.repeat(bad, new), -1, slots)
+    pool.append(rows(rng, slots.size, 2, 128, 1.0), rows(rng, slots.size, 2, 128, 1.0), pos,
+                pkv.rotary_turns(128).numpy(), slots, rows(rng, slots.size, 2, 128))
 
 
 def test_several_runs_and_padding():
