@@ -229,7 +229,8 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     p.cap_log2 = softcap * kLog2e;
     p.window = window;
     p.whole = pl.whole;
-    p.scale_vec = fp8 && pl.HG == 8 && aligned(k_scale, 8) && aligned(v_scale, 8);
+    p.scale_vec = fp8 && (pl.HG == 8 || pl.HG == 4 || pl.HG == 2) &&
+                  aligned(k_scale, pl.HG) && aligned(v_scale, pl.HG);
     return pkv::launch_scored(pl, p, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;

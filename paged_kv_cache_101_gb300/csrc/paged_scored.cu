@@ -65,8 +65,7 @@ struct Ring {
 
 __device__ __forceinline__ Ring carve(uint8_t *raw, const DecodeParams &d)
 {
-    uint8_t *base =
-        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *base = raw + (-smem_u32(raw) & 1023u);  // (as an offset: it stays a shared address)
     Ring r;
     r.stages = base;
     r.hdr = reinterpret_cast<Header *>(base + size_t(d.nst) * d.stage_bytes);
@@ -115,6 +114,88 @@ __device__ __forceinline__ float two_to(int e)
 }
 
 // ------------------------------------------------------------------ producer
+// The blocks of a segment from the newest down, 32 at a time, a lane each: table entries
+// and, for block-scaled pools, their heads' scale bytes. The batch behind the current one
+// is on its way: its entries are asked for when the current batch starts, its scales (they
+// need the entries) when half of that is used. An entry outside the pool is flagged and
+// becomes the block past the pool's end, which TMA reads as zeros (the smallest scale).
+template <bool FP8>
+struct Blocks {
+    int tab = -1, phys = 0;             // lane l: block tab - l
+    uint2 ks, vs;
+    int next_tab = -1, next_phys = 0;   // the batch behind it (-1: none)
+    uint2 next_ks, next_vs;
+    bool scaled = false;                // has next its scales?
+
+    __device__ __forceinline__ int entry(const ScoredParams &p, int s, int top, int b0, int lane)
+    {
+        return top - lane >= b0 ? __ldg(p.d.block_tables + int64_t(s) * p.d.MB + top - lane) : 0;
+    }
+    __device__ __forceinline__ void scales(const ScoredParams &p, int hg, int &id, uint2 &k, uint2 &v)
+    {
+        const DecodeParams &d = p.d;
+        if (id < 0 || id >= d.num_blocks) {
+            atomicOr(d.ws + kWsErr, kErrBadBlock);
+            id = int(d.num_blocks);
+        }
+        if (!FP8)
+            return;
+        k = v = make_uint2(0x01010101u, 0x01010101u);
+        if (id >= d.num_blocks)
+            return;
+        const int64_t at = int64_t(id) * d.Hkv + hg * d.HG;
+        const uint8_t *kp = p.k_scale + at, *vp = p.v_scale + at;
+        if (p.scale_vec && d.HG == 8) {
+            k = __ldg(reinterpret_cast<const uint2 *>(kp));
+            v = __ldg(reinterpret_cast<const uint2 *>(vp));
+        } else if (p.scale_vec && d.HG == 4) {
+            k.x = __ldg(reinterpret_cast<const uint32_t *>(kp));
+            v.x = __ldg(reinterpret_cast<const uint32_t *>(vp));
+        } else if (p.scale_vec && d.HG == 2) {
+            k.x = __ldg(reinterpret_cast<const uint16_t *>(kp));
+            v.x = __ldg(reinterpret_cast<const uint16_t *>(vp));
+        } else {
+            uint32_t kb[8], vb[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                kb[h] = h < d.HG ? __ldg(kp + h) : 0u;
+                vb[h] = h < d.HG ? __ldg(vp + h) : 0u;
+            }
+            k = make_uint2(kb[0] | kb[1] << 8 | kb[2] << 16 | kb[3] << 24,
+                           kb[4] | kb[5] << 8 | kb[6] << 16 | kb[7] << 24);
+            v = make_uint2(vb[0] | vb[1] << 8 | vb[2] << 16 | vb[3] << 24,
+                           vb[4] | vb[5] << 8 | vb[6] << 16 | vb[7] << 24);
+        }
+    }
+    // another segment
+    __device__ __forceinline__ void reset() { tab = next_tab = -1; }
+    // block b is the next one taken
+    __device__ __forceinline__ void reach(const ScoredParams &p, int s, int hg, int b, int b0,
+                                          int lane)
+    {
+        if (tab < 0 || b <= tab - 32) {
+            if (next_tab == b) {
+                if (!scaled)
+                    scales(p, hg, next_phys, next_ks, next_vs);
+                phys = next_phys;
+                ks = next_ks;
+                vs = next_vs;
+            } else {
+                phys = entry(p, s, b, b0, lane);
+                scales(p, hg, phys, ks, vs);
+            }
+            tab = b;
+            next_tab = tab - 32 >= b0 ? tab - 32 : -1;
+            scaled = false;
+            if (next_tab >= 0)
+                next_phys = entry(p, s, next_tab, b0, lane);
+        } else if (next_tab >= 0 && !scaled && b <= tab - 16) {
+            scales(p, hg, next_phys, next_ks, next_vs);
+            scaled = true;
+        }
+    }
+};
+
 template <bool FP8>
 __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const ScoredParams &p,
                          const Ring &ring, int lane)
@@ -192,49 +273,20 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
         Span sp = span(p, s);
         b = sp.b0 + sp.nb - 1 - b;  // the newest block comes first
         const uint64_t policy = policy_evict_first();
-        const bool vec = FP8 && p.scale_vec;
         bool opens = true;        // no segment of this cell ended yet
         bool from_top = false;    // the segment opens its sequence
-        int tab = -1;             // newest of the 32 blocks whose table entries the lanes hold
-        int phys = 0;
-        uint2 ks = make_uint2(0, 0), vs = make_uint2(0, 0);
+        Blocks<FP8> blk;
         for (int64_t u = a; u < e; ++u) {
             const int b_top = sp.b0 + sp.nb - 1;
-            if (b <= tab - 32 || tab < 0) {
-                tab = b;
-                phys = b - lane >= sp.b0 ? __ldg(d.block_tables + int64_t(s) * d.MB + b - lane) : 0;
-                if (phys < 0 || phys >= d.num_blocks) {
-                    atomicOr(d.ws + kWsErr, kErrBadBlock);
-                    phys = int(d.num_blocks);  // past the tensor's end: zeros
-                }
-                if (FP8) {
-                    // the scale bytes of the lane's block (the smallest scale for no block)
-                    ks = vs = make_uint2(0x01010101u, 0x01010101u);
-                    if (phys < d.num_blocks) {
-                        const int64_t at = int64_t(phys) * d.Hkv + hg * d.HG;
-                        if (vec) {
-                            ks = __ldg(reinterpret_cast<const uint2 *>(p.k_scale + at));
-                            vs = __ldg(reinterpret_cast<const uint2 *>(p.v_scale + at));
-                        } else {
-                            uint64_t kw = 0, vw = 0;
-                            for (int h = d.HG - 1; h >= 0; --h) {
-                                kw = kw << 8 | __ldg(p.k_scale + at + h);
-                                vw = vw << 8 | __ldg(p.v_scale + at + h);
-                            }
-                            ks = make_uint2(uint32_t(kw), uint32_t(kw >> 32));
-                            vs = make_uint2(uint32_t(vw), uint32_t(vw >> 32));
-                        }
-                    }
-                }
-            }
-            const int src = tab - b;
-            const int block = __shfl_sync(kFull, phys, src);
+            blk.reach(p, s, hg, b, sp.b0, lane);
+            const int src = blk.tab - b;
+            const int block = __shfl_sync(kFull, blk.phys, src);
             uint4 scales = make_uint4(0, 0, 0, 0);
             if (FP8) {
-                scales.x = __shfl_sync(kFull, ks.x, src);
-                scales.y = __shfl_sync(kFull, ks.y, src);
-                scales.z = __shfl_sync(kFull, vs.x, src);
-                scales.w = __shfl_sync(kFull, vs.y, src);
+                scales.x = __shfl_sync(kFull, blk.ks.x, src);
+                scales.y = __shfl_sync(kFull, blk.ks.y, src);
+                scales.z = __shfl_sync(kFull, blk.vs.x, src);
+                scales.w = __shfl_sync(kFull, blk.vs.y, src);
             }
             const bool first = u == a || b == b_top;
             if (first)
@@ -280,7 +332,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                     sp = span(p, s);
                 } while (sp.nb == 0);
                 b = sp.b0 + sp.nb - 1;
-                tab = -1;
+                blk.reset();
             }
         }
     }

@@ -45,7 +45,7 @@ struct ScoredParams {
     float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
     int whole;               // 1: CTA c has sequence c % S of head group c / S to itself
-    int scale_vec;           // the scale bytes of a block's heads are an aligned 8-byte word
+    int scale_vec;           // the scale bytes of a block's 2, 4 or 8 heads are one aligned word
 };
 
 struct ScoredPlan : DecodePlan {
