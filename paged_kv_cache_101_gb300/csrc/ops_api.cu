@@ -229,6 +229,8 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     p.cap_log2 = softcap * kLog2e;
     p.window = window;
     p.whole = pl.whole;
+    p.teams = pl.teams;
+    p.cells = pl.grid;
     p.scale_vec = fp8 && (pl.HG == 8 || pl.HG == 4 || pl.HG == 2) &&
                   aligned(k_scale, pl.HG) && aligned(v_scale, pl.HG);
     return pkv::launch_scored(pl, p, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -57,21 +57,34 @@ struct Header {
 };
 static_assert(sizeof(Header) == 48, "three 16-byte words");
 
+// A team's ring, and which of all cells is the team's.
 struct Ring {
     uint8_t *stages;
     Header *hdr;
     uint64_t *full, *empty;
+    int cell;
 };
 
-__device__ __forceinline__ Ring carve(uint8_t *raw, const DecodeParams &d)
+__device__ __forceinline__ Ring carve(uint8_t *raw, const ScoredParams &p, int team)
 {
+    const DecodeParams &d = p.d;
     uint8_t *base = raw + (-smem_u32(raw) & 1023u);  // (as an offset: it stays a shared address)
+    const int all = p.teams * d.nst, mine = team * d.nst;
     Ring r;
-    r.stages = base;
-    r.hdr = reinterpret_cast<Header *>(base + size_t(d.nst) * d.stage_bytes);
-    r.full = reinterpret_cast<uint64_t *>(r.hdr + d.nst);
+    r.stages = base + size_t(mine) * d.stage_bytes;
+    r.hdr = reinterpret_cast<Header *>(base + size_t(all) * d.stage_bytes) + mine;
+    r.full = reinterpret_cast<uint64_t *>(base + size_t(all) * (d.stage_bytes + sizeof(Header))) +
+             2 * mine;
     r.empty = r.full + d.nst;
+    r.cell = team * int(gridDim.x) + int(blockIdx.x);
     return r;
+}
+
+// The queries of the teams' consumer warps, behind the rings.
+__device__ __forceinline__ uint8_t *query_fragments(uint8_t *raw, const ScoredParams &p)
+{
+    return raw + (-smem_u32(raw) & 1023u) +
+           size_t(p.teams * p.d.nst) * (p.d.stage_bytes + sizeof(Header) + 16);
 }
 
 // Position in the ring.
@@ -214,19 +227,19 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     Cells C;
     C.F = C.F1 = int64_t(d.n_hg) * total;
     C.F2 = 0;
-    C.G = int(gridDim.x);
+    C.G = p.cells;
     C.NT = 0;
-    if (blockIdx.x == 0 && lane == 0 && !p.whole) {
+    if (ring.cell == 0 && lane == 0 && !p.whole) {
         d.ws[kWsUnits] = uint32_t(total);
         d.ws[kWsDense] = C.F >= C.G ? 1u : 0u;
     }
     int64_t a, e;
     if (p.whole) {
         a = 0;
-        e = span(p, int(blockIdx.x) % S).nb;
+        e = ring.cell < p.cells ? span(p, ring.cell % S).nb : 0;
     } else {
-        a = C.start(blockIdx.x);
-        e = C.start(int64_t(blockIdx.x) + 1);
+        a = C.start(ring.cell);
+        e = C.start(int64_t(ring.cell) + 1);
     }
     Turn turn;
     uint32_t issued = 0;
@@ -245,8 +258,8 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     if (a < e) {
         int hg, s = 0, b = 0;
         if (p.whole) {
-            hg = int(blockIdx.x) / S;
-            s = int(blockIdx.x) - hg * S;
+            hg = ring.cell / S;
+            s = ring.cell - hg * S;
         } else {
             // the sequence that holds unit `rest` of its head group
             hg = int(a / total);
@@ -300,15 +313,15 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                 if (!p.whole) {
                     int2 *rec = d.pieces + int64_t(s) * d.n_hg + hg;
                     if (b == b_top)
-                        rec->x = int(blockIdx.x) * 2 + (opens ? 0 : 1);
+                        rec->x = ring.cell * 2 + (opens ? 0 : 1);
                     if (ends)
-                        rec->y = int(blockIdx.x);
+                        rec->y = ring.cell;
                 }
                 const int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) |
                                   (ends && from_top ? F_DIRECT : 0);
                 int4 *h = reinterpret_cast<int4 *>(&ring.hdr[turn.st]);
                 h[0] = make_int4(s, b, sp.T, hg);
-                h[1] = make_int4(flags, int(blockIdx.x), opens ? 0 : 1, 0);
+                h[1] = make_int4(flags, ring.cell, opens ? 0 : 1, 0);
                 if (FP8)
                     reinterpret_cast<uint4 *>(h)[2] = scales;
                 const uint32_t bar = smem_u32(&ring.full[turn.st]);
@@ -369,13 +382,13 @@ constexpr float kLead = 8.f;
 // E4M3: weights are scaled by 2^6 (at most 2^14 with the lead; f16 ends at 2^16)
 constexpr int kWeightBits = 6;
 
-// A whole-sequence CTA whose sequence has no token: zeros for its heads.
+// A whole-sequence cell whose sequence has no token: zeros for its heads.
 template <int D>
-__device__ __forceinline__ void clear_empty(const ScoredParams &p, int tid, int threads)
+__device__ __forceinline__ void clear_empty(const ScoredParams &p, int cell, int tid, int threads)
 {
     const DecodeParams &d = p.d;
-    const int hg = int(blockIdx.x) / d.S, s = int(blockIdx.x) - hg * d.S;
-    if (seq_tokens(d, s) > 0)
+    const int hg = cell / d.S, s = cell - hg * d.S;
+    if (cell >= p.cells || seq_tokens(d, s) > 0)
         return;
     const int row = d.HG * d.G * D / (d.out_f32 ? 4 : 8);  // 16-byte words
     for (int e = tid; e < d.nq * row; e += threads) {
@@ -387,9 +400,23 @@ __device__ __forceinline__ void clear_empty(const ScoredParams &p, int tid, int 
 
 // The rows of a warp: NT n-tiles of 8, a lane holding rows 2 tq and 2 tq + 1 of each,
 // tokens g and g + 8 of each of up to BL blocks.
+// Above 16 rows a head takes several warps (WPH) of 16 rows. Those wait for their own
+// results most of the time (with 8 warps on an SM the issue slots were 38% busy, the tensor
+// cores 26%), so an SM has twelve of them, in teams of up to four with a ring, a producer
+// warp and a cell each. The registers for that come from the producers (setmaxnreg) and
+// from the queries, which a warp keeps in shared memory.
+constexpr __host__ __device__ bool teams_of(int wph) { return wph > 1; }
+constexpr int kTeamWarps = 12, kMaxTeams = 4;
+constexpr int kTeamThreads = 32 * (kTeamWarps + kMaxTeams);
+constexpr int kLaunchRegs = 128, kConsumerRegs = 152, kProducerRegs = 56;
+static_assert(kTeamWarps * kConsumerRegs + kMaxTeams * kProducerRegs <=
+                  (kTeamWarps + kMaxTeams) * kLaunchRegs,
+              "a block shares out the registers that it was launched with");
+
 template <int D, bool FP8, int NT, int WPH>
-__device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane)
+__device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane, uint8_t *qs)
 {
+    constexpr bool QS = teams_of(WPH);  // queries in shared memory
     constexpr int RL = 2 * NT;       // rows of a lane
     constexpr int BL = FP8 ? 2 : 1;  // blocks of a step: two chains hide each other's waits
     constexpr int NH = FP8 ? 1 : D / 64;
@@ -403,7 +430,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
     const int v_tok = (lane & 7) + ((lane >> 4) & 1) * 8, v_chunk = (lane >> 3) & 1;
     const int sw = lane & 7;
 
-    uint32_t qf[NT][KS][2];
+    uint32_t qf[NT][QS ? 1 : KS][2];
     float acc[MT][NT][4];
     float m_r[RL], l_r[RL], mul[RL], slope[RL];
     int row_j[RL];  // query index of each row (the last one for rows past the end)
@@ -436,7 +463,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         if (flags & F_END)
             break;
         const Header *hb = two ? &ring.hdr[turn2.st] : h;
-        const int s = h->s, T = h->T, b = h->b, kvh = h->hg * d.HG + hl;
+        const int s = h->s, T = h->T, blk = h->b, kvh = h->hg * d.HG + hl;
         const int end_flags = hb->flags, e_cell = h->cell, e_slot = h->slot;
 
         if (flags & F_FIRST) {
@@ -467,6 +494,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 const bool valid = row < d.rows;
                 const uint16_t *q =
                     d.q + ((int64_t(s) * d.nq + j) * d.Hq + int64_t(kvh) * d.G + row - j * d.G) * D;
+                uint32_t qw[KS][2];
                 if constexpr (FP8) {
                     // k-step ks is 16-byte chunk ks of a code row: lane tq holds dims
                     // 16 ks + 4 tq .. + 3 (k 2tq, 2tq + 1, 2tq + 8, 2tq + 9)
@@ -476,8 +504,8 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                         const uint2 w = valid ? __ldg(reinterpret_cast<const uint2 *>(
                                                     q + 16 * ks + 4 * tq))
                                               : make_uint2(0, 0);
-                        qf[nt][ks][0] = w.x;
-                        qf[nt][ks][1] = w.y;
+                        qw[ks][0] = w.x;
+                        qw[ks][1] = w.y;
                         top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo_f32(w.x)), fabsf(bf16hi_f32(w.x))),
                                                fmaxf(fabsf(bf16lo_f32(w.y)), fabsf(bf16hi_f32(w.y)))));
                     }
@@ -491,8 +519,8 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            qf[nt][ks][c] = pack_f16x2(bf16lo_f32(qf[nt][ks][c]) * f,
-                                                       bf16hi_f32(qf[nt][ks][c]) * f);
+                            qw[ks][c] =
+                                pack_f16x2(bf16lo_f32(qw[ks][c]) * f, bf16hi_f32(qw[ks][c]) * f);
                     // the factors of the lane's own rows; not a number where a row holds an
                     // infinity (its products overflow f16)
                     const float back = e > 113 ? NAN : two_to(e);
@@ -502,60 +530,93 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                     const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        qf[nt][ks][0] = valid ? __ldg(w + ks * 8 + tq) : 0u;
-                        qf[nt][ks][1] = valid ? __ldg(w + ks * 8 + 4 + tq) : 0u;
+                        qw[ks][0] = valid ? __ldg(w + ks * 8 + tq) : 0u;
+                        qw[ks][1] = valid ? __ldg(w + ks * 8 + 4 + tq) : 0u;
                     }
+                }
+                if constexpr (QS) {
+                    // (every lane reads back its own words)
+#pragma unroll
+                    for (int i = 0; i < KS / 2; ++i)
+                        reinterpret_cast<uint4 *>(qs)[(i * NT + nt) * 32 + lane] = make_uint4(
+                            qw[2 * i][0], qw[2 * i][1], qw[2 * i + 1][0], qw[2 * i + 1][1]);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            qf[nt][ks][c] = qw[ks][c];
                 }
             }
         }
 
-        // ---- scores S^T[token][row]
+        // ---- scores S^T[token][row] (without a second block, the first one's again: its
+        //      scores are masked below)
         float sc[BL][NT][4];
+        uint32_t kb[BL];
 #pragma unroll
         for (int k = 0; k < BL; ++k) {
+            kb[k] = stages + (k && two ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
+                    uint32_t(hl * NH * kTileBytes);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     sc[k][nt][c] = 0.f;
-            if (k == 1 && !two)
-                break;
-            const uint32_t kb = stages + (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
-                                uint32_t(hl * NH * kTileBytes);
-            if constexpr (FP8) {
-                // one ldmatrix brings chunks 2i and 2i + 1 of all 16 tokens
+        }
 #pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {
-                    uint32_t r[4], a0[4], a1[4];
-                    ldsm_x4(kb + uint32_t(k_tok * 128 + (((2 * i + k_chunk) ^ sw) << 4)), r);
+        for (int i = 0; i < KS / 2; ++i) {  // k-steps 2i, 2i + 1
+            uint32_t b[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (QS) {
+                    const uint4 w = reinterpret_cast<const uint4 *>(qs)[(i * NT + nt) * 32 + lane];
+                    b[nt][0] = w.x;
+                    b[nt][1] = w.y;
+                    b[nt][2] = w.z;
+                    b[nt][3] = w.w;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        b[nt][c] = qf[nt][2 * i + (c >> 1)][c & 1];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BL; ++k) {
+                uint32_t a0[4], a1[4];
+                if constexpr (FP8) {
+                    // one ldmatrix brings chunks 2i and 2i + 1 of all 16 tokens
+                    uint32_t r[4];
+                    ldsm_x4(kb[k] + uint32_t(k_tok * 128 + (((2 * i + k_chunk) ^ sw) << 4)), r);
                     e4m3x4_to_f16x2x2(r[0], a0[0], a0[2]);
                     e4m3x4_to_f16x2x2(r[1], a0[1], a0[3]);
                     e4m3x4_to_f16x2x2(r[2], a1[0], a1[2]);
                     e4m3x4_to_f16x2x2(r[3], a1[1], a1[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16_16816(sc[k][nt], a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-                        mma_f16_16816(sc[k][nt], a1, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
-                    }
+                } else {
+                    const int c0 = 4 * i + k_chunk, c1 = c0 + 2;
+                    ldsm_x4(kb[k] + uint32_t((c0 >> 3) * kTileBytes + k_tok * 128 +
+                                             (((c0 & 7) ^ sw) << 4)),
+                            a0);
+                    ldsm_x4(kb[k] + uint32_t((c1 >> 3) * kTileBytes + k_tok * 128 +
+                                             (((c1 & 7) ^ sw) << 4)),
+                            a1);
                 }
-            } else {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int chunk = 2 * ks + k_chunk;
-                    uint32_t a[4];
-                    ldsm_x4(kb + uint32_t((chunk >> 3) * kTileBytes + k_tok * 128 +
-                                          (((chunk & 7) ^ sw) << 4)),
-                            a);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_bf16_16816(sc[k][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (FP8) {
+                        mma_f16_16816(sc[k][nt], a0, b[nt][0], b[nt][1]);
+                        mma_f16_16816(sc[k][nt], a1, b[nt][2], b[nt][3]);
+                    } else {
+                        mma_bf16_16816(sc[k][nt], a0, b[nt][0], b[nt][1]);
+                        mma_bf16_16816(sc[k][nt], a1, b[nt][2], b[nt][3]);
+                    }
                 }
             }
         }
 
         // ---- into y = x log2(e): x[k][i][c] is row i, block b - k, token g + 8 c
         float x[BL][RL][2];
-        const int t0 = b * kBlockSize;                          // the newer block
+        const int t0 = blk * kBlockSize;                          // the newer block
         const int t_low = two ? t0 - kBlockSize : t0;           // the step's first token
         const int first = first_seen(p, T);
         // are all tokens of the step seen by all rows?
@@ -819,31 +880,45 @@ constexpr int kConsumers = 8;
 constexpr int64_t kWholeBytes = 256 * 1024;
 
 template <int D, bool FP8, int NT, int WPH>
-__global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
+__global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumers + 1), 1)
     scored_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ ScoredParams p)
 {
+    constexpr bool TEAMS = teams_of(WPH);
     extern __shared__ uint8_t smem_raw[];
-    const Ring ring = carve(smem_raw, p.d);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // consumer warps of a team lie together; producers behind all of them
+    const bool produces = warp >= (TEAMS ? kTeamWarps : p.d.ncw);
+    const int team = !TEAMS ? 0 : produces ? warp - kTeamWarps : warp / p.d.ncw;
+    const Ring ring = carve(smem_raw, p, team);
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
-        for (int i = 0; i < p.d.nst; ++i) {
-            mbar_init(smem_u32(&ring.full[i]), 1);
-            mbar_init(smem_u32(&ring.empty[i]), uint32_t(p.d.ncw));
-        }
+        for (int t = 0; t < p.teams; ++t)
+            for (int i = 0; i < p.d.nst; ++i) {
+                mbar_init(smem_u32(&ring.full[2 * t * p.d.nst + i]), 1);
+                mbar_init(smem_u32(&ring.empty[2 * t * p.d.nst + i]), uint32_t(p.d.ncw));
+            }
         fence_mbar_init();
     }
     // the kernel before this one on the stream may still write q or the pools
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
-    if (warp == p.d.ncw)
-        producer<FP8>(&kmap, &vmap, p, ring, lane);
-    else {
-        if (p.whole)
-            clear_empty<D>(p, threadIdx.x, 32 * p.d.ncw);
-        consumer<D, FP8, NT, WPH>(p, ring, warp, lane);
+    if (produces) {
+        if constexpr (TEAMS)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        if (team < p.teams)
+            producer<FP8>(&kmap, &vmap, p, ring, lane);
+    } else {
+        if constexpr (TEAMS)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+        if (team < p.teams) {
+            const int cw = TEAMS ? warp - team * p.d.ncw : warp;
+            if (p.whole)
+                clear_empty<D>(p, ring.cell, cw * 32 + lane, 32 * p.d.ncw);
+            consumer<D, FP8, NT, WPH>(p, ring, cw, lane,
+                                      query_fragments(smem_raw, p) + warp * (NT * D * 16));
+        }
     }
 }
 
@@ -854,12 +929,21 @@ cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtens
                        const CUtensorMap &vmap, cudaStream_t stream)
 {
     const auto kern = scored_kernel<D, FP8, NT, WPH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e;
+    if (teams_of(WPH)) {
+        // the warps share out kLaunchRegs a thread: with fewer they would wait forever
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess)
+            return e;
+        if (fa.numRegs < kLaunchRegs)
+            return cudaErrorLaunchOutOfResources;
+    }
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(pl.smem));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(pl.grid));
+    cfg.gridDim = dim3(unsigned(pl.ctas));
     cfg.blockDim = dim3(unsigned(pl.threads));
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
@@ -889,29 +973,35 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     P.ntw = tiles == 1 ? 1 : 2;
     P.wph = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
     P.rows_pad = P.wph * P.ntw * 8;
+    const bool teams = teams_of(P.wph);
     P.HG = 1;
-    for (int h = std::min(kConsumers / P.wph, Hkv); h >= 1; --h)
+    for (int h = std::min((teams ? kTeamWarps / 3 : kConsumers) / P.wph, Hkv); h >= 1; --h)
         if (Hkv % h == 0) {
             P.HG = h;
             break;
         }
     P.n_hg = Hkv / P.HG;
-    P.threads = 32 * (1 + P.HG * P.wph);
+    const int ncw = P.HG * P.wph;
+    P.teams = teams ? std::min(kMaxTeams, kTeamWarps / ncw) : 1;
+    P.threads = teams ? kTeamThreads : 32 * (1 + ncw);
     P.stage_bytes = 2 * P.HG * (fp8 ? 1 : D / 64) * kTileBytes;
     // few heads: several CTAs share an SM, so that as many warps hide each other's waits
-    P.ctas_per_sm = std::min(4, std::max(1, kConsumers / (P.HG * P.wph)));
+    P.ctas_per_sm = teams ? 1 : std::min(4, std::max(1, kConsumers / ncw));
     const int per_stage = P.stage_bytes + int(sizeof(Header)) + 16;
+    const int queries = teams ? P.teams * ncw * P.ntw * D * 16 : 0;
     const int budget = P.ctas_per_sm == 1 ? smem_optin : (smem_optin + 1024) / P.ctas_per_sm - 1024;
-    P.nst = std::min(16, (budget - 1024) / per_stage);
+    P.nst = std::min(16, (budget - 1024 - queries) / per_stage / P.teams);
     if (P.nst < 3)
         return -1;
-    P.smem = 1024 + size_t(P.nst) * per_stage;
-    const int cap = P.ctas_per_sm * num_sms;
-    P.grid = int(std::min<int64_t>(cap, int64_t(P.n_hg) * S * MB));
-    // few and short sequences: one CTA each, no second launch to join pieces
+    P.smem = 1024 + size_t(P.teams) * P.nst * per_stage + queries;
+    const int cap = P.ctas_per_sm * num_sms * P.teams;  // cells at most
+    P.ctas = int(std::min<int64_t>(P.ctas_per_sm * num_sms, int64_t(P.n_hg) * S * MB));
+    P.grid = P.ctas * P.teams;
+    // few and short sequences: one cell each, no second launch to join pieces
     if (int64_t(P.n_hg) * S <= cap && int64_t(MB) * P.stage_bytes <= kWholeBytes) {
         P.whole = 1;
         P.grid = P.n_hg * S;
+        P.ctas = std::min(P.ctas_per_sm * num_sms, P.grid);
     }
     P.off_rec = kWsHeaderBytes;
     P.off_ml = P.off_rec + round_up(size_t(S) * P.n_hg * 8, 256);

@@ -44,12 +44,15 @@ struct ScoredParams {
     float mul;               // to the log2 domain: scale log2(e), or 2 scale log2(e) / softcap
     float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
-    int whole;               // 1: CTA c has sequence c % S of head group c / S to itself
+    int whole;               // 1: cell c is sequence c % S of head group c / S
+    int teams, cells;        // as in the plan
     int scale_vec;           // the scale bytes of a block's 2, 4 or 8 heads are one aligned word
 };
 
-struct ScoredPlan : DecodePlan {
-    int whole;  // every CTA has a sequence of a head group to itself: no pieces, no merge
+struct ScoredPlan : DecodePlan {  // (grid: the cells of the call)
+    int whole;  // every cell is a sequence of a head group: no pieces, no merge
+    int teams;  // cells that a CTA works on at a time, each with warps and a ring of its own
+    int ctas;   // of the launch
 };
 
 // The plan of a scored call (fp8: block-scaled pools), MB the most blocks that a
