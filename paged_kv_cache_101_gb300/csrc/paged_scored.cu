@@ -48,14 +48,19 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// One stage's block: which sequence and logical block, what part it plays in its
-// segment (F_*), and the scale bytes of its heads.
+// Blocks of a stage. A wait for a barrier that has long completed costs a warp 83 cycles,
+// and as much again goes into headers and hand-backs: E4M3 blocks come in pairs (two bf16
+// blocks would leave too few stages).
+constexpr __host__ __device__ int stage_blocks(bool fp8) { return fp8 ? 2 : 1; }
+
+// One stage's n blocks b, b - 1: their sequence, what part they play in its segment (F_*),
+// and the scale bytes of their heads.
 struct Header {
     int32_t s, b, T, hg;
-    int32_t flags, cell, slot, unused;
-    uint8_t ks[8], vs[8];
+    int32_t flags, cell, slot, n;
+    uint8_t ks[2][8], vs[2][8];
 };
-static_assert(sizeof(Header) == 48, "three 16-byte words");
+static_assert(sizeof(Header) == 64, "four 16-byte words");
 
 // A team's ring, and which of all cells is the team's.
 struct Ring {
@@ -182,11 +187,11 @@ struct Blocks {
     }
     // another segment
     __device__ __forceinline__ void reset() { tab = next_tab = -1; }
-    // block b is the next one taken
-    __device__ __forceinline__ void reach(const ScoredParams &p, int s, int hg, int b, int b0,
-                                          int lane)
+    // blocks b .. b - n + 1 are the next ones taken (all n before them were the same)
+    __device__ __forceinline__ void reach(const ScoredParams &p, int s, int hg, int b, int n,
+                                          int b0, int lane)
     {
-        if (tab < 0 || b <= tab - 32) {
+        if (tab < 0 || b - n < tab - 32) {
             if (next_tab == b) {
                 if (!scaled)
                     scales(p, hg, next_phys, next_ks, next_vs);
@@ -213,6 +218,7 @@ template <bool FP8>
 __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const ScoredParams &p,
                          const Ring &ring, int lane)
 {
+    constexpr int BL = stage_blocks(FP8);
     const DecodeParams &d = p.d;
     const int S = d.S;
     int64_t total = 0;
@@ -289,22 +295,27 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
         bool opens = true;        // no segment of this cell ended yet
         bool from_top = false;    // the segment opens its sequence
         Blocks<FP8> blk;
-        for (int64_t u = a; u < e; ++u) {
+        for (int64_t u = a; u < e;) {
             const int b_top = sp.b0 + sp.nb - 1;
-            blk.reach(p, s, hg, b, sp.b0, lane);
+            const int n = BL == 2 && u + 1 < e && b > sp.b0 ? 2 : 1;
+            blk.reach(p, s, hg, b, n, sp.b0, lane);
             const int src = blk.tab - b;
-            const int block = __shfl_sync(kFull, blk.phys, src);
-            uint4 scales = make_uint4(0, 0, 0, 0);
-            if (FP8) {
-                scales.x = __shfl_sync(kFull, blk.ks.x, src);
-                scales.y = __shfl_sync(kFull, blk.ks.y, src);
-                scales.z = __shfl_sync(kFull, blk.vs.x, src);
-                scales.w = __shfl_sync(kFull, blk.vs.y, src);
+            int block[BL];
+            uint2 ks[BL], vs[BL];
+#pragma unroll
+            for (int k = 0; k < BL; ++k) {
+                block[k] = __shfl_sync(kFull, blk.phys, src + k);
+                if (FP8) {
+                    ks[k].x = __shfl_sync(kFull, blk.ks.x, src + k);
+                    ks[k].y = __shfl_sync(kFull, blk.ks.y, src + k);
+                    vs[k].x = __shfl_sync(kFull, blk.vs.x, src + k);
+                    vs[k].y = __shfl_sync(kFull, blk.vs.y, src + k);
+                }
             }
             const bool first = u == a || b == b_top;
             if (first)
                 from_top = b == b_top;
-            const bool ends = b == sp.b0, last = u == e - 1 || ends;
+            const bool ends = b - n < sp.b0, last = u + n == e || ends;
             if (!(ok = acquire()))
                 break;
             if (lane == 0) {
@@ -319,24 +330,33 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
                 }
                 const int flags = (first ? F_FIRST : 0) | (last ? F_LAST : 0) |
                                   (ends && from_top ? F_DIRECT : 0);
-                int4 *h = reinterpret_cast<int4 *>(&ring.hdr[turn.st]);
-                h[0] = make_int4(s, b, sp.T, hg);
-                h[1] = make_int4(flags, ring.cell, opens ? 0 : 1, 0);
-                if (FP8)
-                    reinterpret_cast<uint4 *>(h)[2] = scales;
+                uint4 *h = reinterpret_cast<uint4 *>(&ring.hdr[turn.st]);
+                h[0] = make_uint4(s, b, sp.T, hg);
+                h[1] = make_uint4(flags, ring.cell, opens ? 0 : 1, n);
+                if constexpr (FP8) {
+                    h[2] = make_uint4(ks[0].x, ks[0].y, ks[1].x, ks[1].y);
+                    h[3] = make_uint4(vs[0].x, vs[0].y, vs[1].x, vs[1].y);
+                }
+                const uint32_t bytes = uint32_t(d.stage_bytes / BL);
                 const uint32_t bar = smem_u32(&ring.full[turn.st]);
-                mbar_arrive_expect_tx(bar, uint32_t(d.stage_bytes));
-                const uint32_t dst = smem_u32(ring.stages + size_t(turn.st) * d.stage_bytes);
-                tma_load_5d_hint(dst, kmap, bar, 0, 0, 0, hg * d.HG, block, policy);
-                tma_load_5d_hint(dst + uint32_t(d.stage_bytes / 2), vmap, bar, 0, 0, 0, hg * d.HG,
-                                 block, policy);
+                mbar_arrive_expect_tx(bar, uint32_t(n) * bytes);
+                uint32_t dst = smem_u32(ring.stages) + turn.st * uint32_t(d.stage_bytes);
+#pragma unroll
+                for (int k = 0; k < BL; ++k, dst += bytes)
+                    if (k < n) {
+                        tma_load_5d_hint(dst, kmap, bar, 0, 0, 0, hg * d.HG, block[k], policy);
+                        tma_load_5d_hint(dst + bytes / 2, vmap, bar, 0, 0, 0, hg * d.HG, block[k],
+                                         policy);
+                    }
             }
             __syncwarp();
             ++issued;
             turn.next(d.nst);
+            u += n;
+            b -= n;
             if (last)
                 opens = false;
-            if (--b < sp.b0 && u + 1 < e) {
+            if (b < sp.b0 && u < e) {
                 do {
                     if (++s == S) {
                         s = 0;
@@ -418,7 +438,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
 {
     constexpr bool QS = teams_of(WPH);  // queries in shared memory
     constexpr int RL = 2 * NT;       // rows of a lane
-    constexpr int BL = FP8 ? 2 : 1;  // blocks of a step: two chains hide each other's waits
+    constexpr int BL = stage_blocks(FP8);  // two chains hide each other's waits
     constexpr int NH = FP8 ? 1 : D / 64;
     constexpr int KS = D / 16;       // k-steps of the scores
     constexpr int MT = D / 16;       // 16-dim m-tiles of the output
@@ -446,25 +466,18 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
     const uint32_t stages = smem_u32(ring.stages);
     Turn turn;
     for (;;) {
-        bool up = mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs);
-        const Header *h = &ring.hdr[turn.st];
-        const int flags = up ? h->flags : F_END;
-        // the next block of the same segment goes along
-        Turn turn2 = turn;
-        turn2.next(d.nst);
-        const bool two = BL == 2 && !(flags & (F_LAST | F_END));
-        if (two)
-            up = mbar_wait(smem_u32(&ring.full[turn2.st]), turn2.phase, kWaitLimitNs);
-        if (!up) {
+        if (!mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs)) {
             if (lane == 0)
                 atomicOr(d.ws + kWsErr, kErrConsumerWait);
             return;
         }
+        const Header *h = &ring.hdr[turn.st];
+        const int flags = h->flags;
         if (flags & F_END)
             break;
-        const Header *hb = two ? &ring.hdr[turn2.st] : h;
         const int s = h->s, T = h->T, blk = h->b, kvh = h->hg * d.HG + hl;
-        const int end_flags = hb->flags, e_cell = h->cell, e_slot = h->slot;
+        const bool two = BL == 2 && h->n == 2;
+        const int e_cell = h->cell, e_slot = h->slot;
 
         if (flags & F_FIRST) {
             // ---- a new segment: empty state, its queries
@@ -550,14 +563,14 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
             }
         }
 
-        // ---- scores S^T[token][row] (without a second block, the first one's again: its
-        //      scores are masked below)
+        // ---- scores S^T[token][row] (of whatever is there, where a second block is missing:
+        //      those are masked below)
         float sc[BL][NT][4];
+        const uint32_t stage = stages + turn.st * uint32_t(d.stage_bytes);
         uint32_t kb[BL];
 #pragma unroll
         for (int k = 0; k < BL; ++k) {
-            kb[k] = stages + (k && two ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
-                    uint32_t(hl * NH * kTileBytes);
+            kb[k] = stage + uint32_t((k * 2 * d.HG + hl) * NH * kTileBytes);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -623,7 +636,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         const bool masked = t0 + kBlockSize - 1 > T - d.nq || (p.window > 0 && t_low < T - p.window);
 #pragma unroll
         for (int k = 0; k < BL; ++k) {
-            const float kf = FP8 ? __uint_as_float(uint32_t((k ? hb : h)->ks[hl]) << 23) : 1.f;
+            const float kf = FP8 ? __uint_as_float(uint32_t(h->ks[k][hl]) << 23) : 1.f;
 #pragma unroll
             for (int i = 0; i < RL; ++i)
 #pragma unroll
@@ -683,8 +696,8 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         }
         int ev[2] = {0, 0}, e_new = 0;
         if constexpr (FP8) {
-            ev[0] = h->vs[hl];
-            ev[1] = hb->vs[hl];
+            ev[0] = h->vs[0][hl];
+            ev[1] = two ? h->vs[1][hl] : 0;
             e_new = max(e_max, max(ev[0], ev[1]));
         }
         if (__any_sync(kFull, lead) || e_new > e_max) {
@@ -762,8 +775,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                                   (t + 1 >= first && t + 1 < T ? 0xffff0000u : 0u);
                     }
                 }
-                const uint32_t vb = stages + (k ? turn2.st : turn.st) * uint32_t(d.stage_bytes) +
-                                    uint32_t((d.HG + hl) * NH * kTileBytes);
+                const uint32_t vb = kb[k] + uint32_t(d.HG * NH * kTileBytes);
                 if constexpr (FP8) {
                     // chunks 2i and 2i + 1: a lane gets tokens 2tq, 2tq + 1 of the code pair
                     // (dims 2g, 2g + 1). Even dims (bytes 0, 2) make m-tile 2i, odd ones
@@ -815,20 +827,15 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         else
             pv(std::false_type());
 
-        // ---- the stages go back to the producer
+        // ---- the stage goes back to the producer
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0)
             mbar_arrive(smem_u32(&ring.empty[turn.st]));
-            if (two)
-                mbar_arrive(smem_u32(&ring.empty[turn2.st]));
-        }
         turn.next(d.nst);
-        if (two)
-            turn.next(d.nst);
 
-        if (end_flags & F_LAST) {
+        if (flags & F_LAST) {
             // ---- the segment's end: full row sums, then the output or a partial
-            const bool direct = end_flags & F_DIRECT;
+            const bool direct = flags & F_DIRECT;
             const float vf = FP8 ? ldexpf(1.f, e_max - 127 - kWeightBits) : 1.f;
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
@@ -984,21 +991,22 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     const int ncw = P.HG * P.wph;
     P.teams = teams ? std::min(kMaxTeams, kTeamWarps / ncw) : 1;
     P.threads = teams ? kTeamThreads : 32 * (1 + ncw);
-    P.stage_bytes = 2 * P.HG * (fp8 ? 1 : D / 64) * kTileBytes;
+    const int block_bytes = 2 * P.HG * (fp8 ? 1 : D / 64) * kTileBytes;
+    P.stage_bytes = stage_blocks(fp8) * block_bytes;
     // few heads: several CTAs share an SM, so that as many warps hide each other's waits
     P.ctas_per_sm = teams ? 1 : std::min(4, std::max(1, kConsumers / ncw));
     const int per_stage = P.stage_bytes + int(sizeof(Header)) + 16;
     const int queries = teams ? P.teams * ncw * P.ntw * D * 16 : 0;
     const int budget = P.ctas_per_sm == 1 ? smem_optin : (smem_optin + 1024) / P.ctas_per_sm - 1024;
     P.nst = std::min(16, (budget - 1024 - queries) / per_stage / P.teams);
-    if (P.nst < 3)
+    if (P.nst < 2)
         return -1;
     P.smem = 1024 + size_t(P.teams) * P.nst * per_stage + queries;
     const int cap = P.ctas_per_sm * num_sms * P.teams;  // cells at most
     P.ctas = int(std::min<int64_t>(P.ctas_per_sm * num_sms, int64_t(P.n_hg) * S * MB));
     P.grid = P.ctas * P.teams;
     // few and short sequences: one cell each, no second launch to join pieces
-    if (int64_t(P.n_hg) * S <= cap && int64_t(MB) * P.stage_bytes <= kWholeBytes) {
+    if (int64_t(P.n_hg) * S <= cap && int64_t(MB) * block_bytes <= kWholeBytes) {
         P.whole = 1;
         P.grid = P.n_hg * S;
         P.ctas = std::min(P.ctas_per_sm * num_sms, P.grid);
