@@ -445,10 +445,17 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
     const DecodeParams &d = p.d;
     const int hl = cw / WPH, r0 = (cw % WPH) * 8 * NT;
     const int g = lane >> 2, tq = lane & 3;
-    // ldmatrix rows inside a [16 tokens][8 x 16 bytes] tile, 128-byte swizzle
+    // ldmatrix rows inside a [16 tokens][8 x 16 bytes] tile, 128-byte swizzle: where the lane
+    // finds chunk 0 or 1; chunks 2i or 2i + 1 are at that address ^ 32 i
     const int k_tok = (lane & 7) + ((lane >> 3) & 1) * 8, k_chunk = lane >> 4;
     const int v_tok = (lane & 7) + ((lane >> 4) & 1) * 8, v_chunk = (lane >> 3) & 1;
     const int sw = lane & 7;
+    const uint32_t k_at = smem_u32(ring.stages) + uint32_t(hl * NH * kTileBytes + k_tok * 128 +
+                                                           ((k_chunk ^ sw) << 4));
+    const uint32_t v_at =
+        smem_u32(ring.stages) +
+        uint32_t((d.HG + hl) * NH * kTileBytes + v_tok * 128 + ((v_chunk ^ sw) << 4));
+    const uint32_t block_bytes = uint32_t(2 * d.HG * NH * kTileBytes);
 
     uint32_t qf[NT][QS ? 1 : KS][2];
     float acc[MT][NT][4];
@@ -463,7 +470,6 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         slope[i] = 0.f;
         mul[i] = p.mul;
     }
-    const uint32_t stages = smem_u32(ring.stages);
     Turn turn;
     for (;;) {
         if (!mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs)) {
@@ -566,11 +572,9 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         // ---- scores S^T[token][row] (of whatever is there, where a second block is missing:
         //      those are masked below)
         float sc[BL][NT][4];
-        const uint32_t stage = stages + turn.st * uint32_t(d.stage_bytes);
-        uint32_t kb[BL];
+        const uint32_t stage = turn.st * uint32_t(d.stage_bytes);
 #pragma unroll
         for (int k = 0; k < BL; ++k) {
-            kb[k] = stage + uint32_t((k * 2 * d.HG + hl) * NH * kTileBytes);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -600,19 +604,15 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 if constexpr (FP8) {
                     // one ldmatrix brings chunks 2i and 2i + 1 of all 16 tokens
                     uint32_t r[4];
-                    ldsm_x4(kb[k] + uint32_t(k_tok * 128 + (((2 * i + k_chunk) ^ sw) << 4)), r);
+                    ldsm_x4((k_at + stage + k * block_bytes) ^ uint32_t(32 * i), r);
                     e4m3x4_to_f16x2x2(r[0], a0[0], a0[2]);
                     e4m3x4_to_f16x2x2(r[1], a0[1], a0[3]);
                     e4m3x4_to_f16x2x2(r[2], a1[0], a1[2]);
                     e4m3x4_to_f16x2x2(r[3], a1[1], a1[3]);
                 } else {
-                    const int c0 = 4 * i + k_chunk, c1 = c0 + 2;
-                    ldsm_x4(kb[k] + uint32_t((c0 >> 3) * kTileBytes + k_tok * 128 +
-                                             (((c0 & 7) ^ sw) << 4)),
-                            a0);
-                    ldsm_x4(kb[k] + uint32_t((c1 >> 3) * kTileBytes + k_tok * 128 +
-                                             (((c1 & 7) ^ sw) << 4)),
-                            a1);
+                    const uint32_t at = k_at + stage + uint32_t((i >> 1) * kTileBytes);
+                    ldsm_x4(at ^ uint32_t(64 * (i & 1)), a0);
+                    ldsm_x4(at ^ uint32_t(64 * (i & 1) + 32), a1);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -775,7 +775,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                                   (t + 1 >= first && t + 1 < T ? 0xffff0000u : 0u);
                     }
                 }
-                const uint32_t vb = kb[k] + uint32_t(d.HG * NH * kTileBytes);
+                const uint32_t vb = v_at + stage + k * block_bytes;
                 if constexpr (FP8) {
                     // chunks 2i and 2i + 1: a lane gets tokens 2tq, 2tq + 1 of the code pair
                     // (dims 2g, 2g + 1). Even dims (bytes 0, 2) make m-tile 2i, odd ones
@@ -783,8 +783,7 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
 #pragma unroll
                     for (int i = 0; i < MT / 2; ++i) {
                         uint32_t r[4], ae[4], ao[4];
-                        ldsm_x4_trans(
-                            vb + uint32_t(v_tok * 128 + (((2 * i + v_chunk) ^ sw) << 4)), r);
+                        ldsm_x4_trans(vb ^ uint32_t(32 * i), r);
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             e4m3x4_to_f16x2x2(__byte_perm(r[m], 0u, 0x3120), ae[m], ao[m]);
@@ -802,10 +801,9 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
                 } else {
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        const int chunk = 2 * i + v_chunk;
                         uint32_t a[4];
-                        ldsm_x4_trans(vb + uint32_t((chunk >> 3) * kTileBytes + v_tok * 128 +
-                                                    (((chunk & 7) ^ sw) << 4)),
+                        ldsm_x4_trans((vb + uint32_t((i >> 2) * kTileBytes)) ^
+                                          uint32_t(32 * (i & 3)),
                                       a);
                         if constexpr (EDGE) {
                             a[0] &= keep[0];
