@@ -428,7 +428,7 @@ __device__ __forceinline__ void clear_empty(const ScoredParams &p, int cell, int
 constexpr __host__ __device__ bool teams_of(int wph) { return wph > 1; }
 constexpr int kTeamWarps = 12, kMaxTeams = 4;
 constexpr int kTeamThreads = 32 * (kTeamWarps + kMaxTeams);
-constexpr int kLaunchRegs = 128, kConsumerRegs = 152, kProducerRegs = 56;
+constexpr int kLaunchRegs = 128, kConsumerRegs = 144, kProducerRegs = 80;
 static_assert(kTeamWarps * kConsumerRegs + kMaxTeams * kProducerRegs <=
                   (kTeamWarps + kMaxTeams) * kLaunchRegs,
               "a block shares out the registers that it was launched with");
