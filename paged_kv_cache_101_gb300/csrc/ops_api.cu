@@ -128,6 +128,8 @@ pkv_status rope_append(pkv::RopeParams &p, int64_t num_blocks, bool fp8, void *s
 }
 
 // ------------------------------------------------------------------ scored attention
+constexpr int kMaxTableWidth = 1 << 26;
+
 pkv_status check_scored_geometry(int32_t num_seqs, int32_t nq, int32_t Hq, int32_t Hkv, int32_t D)
 {
     if (num_seqs < 0 || nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
@@ -169,7 +171,7 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(slopes, 4) ||
         !aligned(workspace, 256))
         return PKV_ERR_ALIGN;
-    if (max_blocks_per_seq > (1 << 26) || num_blocks > 0x7fffffffLL || num_seqs > (1 << 24) ||
+    if (max_blocks_per_seq > kMaxTableWidth || num_blocks > 0x7fffffffLL || num_seqs > (1 << 24) ||
         Hkv > 65535)
         return PKV_ERR_RANGE;
     DeviceLimits dev;
@@ -231,6 +233,7 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     p.whole = pl.whole;
     p.teams = pl.teams;
     p.cells = pl.grid;
+    p.cluster = pl.cluster;
     p.scale_vec = fp8 && (pl.HG == 8 || pl.HG == 4 || pl.HG == 2) &&
                   aligned(k_scale, pl.HG) && aligned(v_scale, pl.HG);
     return pkv::launch_scored(pl, p, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -318,13 +321,14 @@ size_t pkv_workspace_size_scored(int32_t num_seqs, int32_t n_query_per_seq, int3
     DeviceLimits dev;
     if (device_limits(&dev) != cudaSuccess)
         return 0;
-    // the larger of the two pool types; a plan's size does not grow with the table width
+    // the larger of the two pool types, at the widest table (the forms for narrow ones need
+    // less, and otherwise the width plays no part)
     size_t bytes = 0;
     for (int fp8 = 0; fp8 < 2; ++fp8) {
         pkv::ScoredPlan pl;
         if ((fp8 && head_dim != 128) ||
-            pkv::plan_scored(num_seqs, n_query_per_seq, num_q_heads, num_kv_heads, head_dim, 1,
-                             dev.sms, dev.smem, fp8, &pl) != 0)
+            pkv::plan_scored(num_seqs, n_query_per_seq, num_q_heads, num_kv_heads, head_dim,
+                             kMaxTableWidth, dev.sms, dev.smem, fp8, &pl) != 0)
             continue;
         bytes = pl.ws_bytes > bytes ? pl.ws_bytes : bytes;
     }

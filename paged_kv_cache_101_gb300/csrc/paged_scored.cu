@@ -70,11 +70,12 @@ struct Ring {
     int cell;
 };
 
-__device__ __forceinline__ Ring carve(uint8_t *raw, const ScoredParams &p, int team)
+
+__device__ __forceinline__ Ring carve(uint8_t *raw, const ScoredParams &p, int rings, int team)
 {
     const DecodeParams &d = p.d;
     uint8_t *base = raw + (-smem_u32(raw) & 1023u);  // (as an offset: it stays a shared address)
-    const int all = p.teams * d.nst, mine = team * d.nst;
+    const int all = rings * d.nst, mine = team * d.nst;
     Ring r;
     r.stages = base + size_t(mine) * d.stage_bytes;
     r.hdr = reinterpret_cast<Header *>(base + size_t(all) * d.stage_bytes) + mine;
@@ -86,10 +87,10 @@ __device__ __forceinline__ Ring carve(uint8_t *raw, const ScoredParams &p, int t
 }
 
 // The queries of the teams' consumer warps, behind the rings.
-__device__ __forceinline__ uint8_t *query_fragments(uint8_t *raw, const ScoredParams &p)
+__device__ __forceinline__ uint8_t *query_fragments(uint8_t *raw, const ScoredParams &p, int rings)
 {
     return raw + (-smem_u32(raw) & 1023u) +
-           size_t(p.teams * p.d.nst) * (p.d.stage_bytes + sizeof(Header) + 16);
+           size_t(rings * p.d.nst) * (p.d.stage_bytes + sizeof(Header) + 16);
 }
 
 // Position in the ring.
@@ -123,6 +124,29 @@ __device__ __forceinline__ Span span(const ScoredParams &p, int s)
     r.b0 = first_seen(p, r.T) / kBlockSize;
     r.nb = (r.T + kBlockSize - 1) / kBlockSize - r.b0;
     return r;
+}
+
+// What a CTA of a cluster (the joined form) takes: stages' worth [lo, hi) of the blocks of
+// sequence s and head h, counted from the newest.
+struct Share {
+    int s, h, rank, lo, hi;
+    Span sp;
+};
+
+template <bool FP8>
+__device__ __forceinline__ Share share(const ScoredParams &p)
+{
+    constexpr int BL = stage_blocks(FP8);
+    Share h;
+    const int id = int(blockIdx.x) / p.cluster;
+    h.rank = int(blockIdx.x) - id * p.cluster;
+    h.h = id / p.d.S;
+    h.s = id - h.h * p.d.S;
+    h.sp = span(p, h.s);
+    const int n = (h.sp.nb + BL - 1) / BL;
+    h.lo = int(int64_t(n) * h.rank / p.cluster);
+    h.hi = int(int64_t(n) * (h.rank + 1) / p.cluster);
+    return h;
 }
 
 // 2^e; 0 below the normal range.
@@ -389,6 +413,110 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     }
 }
 
+// The joined form's producer: lane t has the stages of team t, so that a turn of all teams
+// costs one stage's instructions. A turn's table entries are asked for two turns ahead, the
+// scale bytes that they point to one turn ahead.
+template <bool FP8>
+__device__ void produce_share(const CUtensorMap *kmap, const CUtensorMap *vmap,
+                              const ScoredParams &p, const Ring &ring, const Share &part, int lane)
+{
+    constexpr int BL = stage_blocks(FP8);
+    const DecodeParams &d = p.d;
+    const int T = p.teams, n = part.hi - part.lo;
+    const int32_t *table = d.block_tables + int64_t(part.s) * d.MB;
+    const int top = part.sp.b0 + part.sp.nb - 1 - part.lo * BL;  // the share's newest block
+    const uint64_t policy = policy_evict_first();
+    const bool works = lane < T;
+    const uint32_t bytes = uint32_t(d.stage_bytes / BL);
+    int id[BL], id2[BL];
+    uint32_t ks[BL], vs[BL];
+
+    // blocks of stage i: top - BL i and the one before it
+    const auto entries = [&](int i, int (&e)[BL]) {
+#pragma unroll
+        for (int k = 0; k < BL; ++k) {
+            const int b = top - BL * i - k;
+            e[k] = works && i < n && b >= part.sp.b0 ? __ldg(table + b) : 0;
+        }
+    };
+    const auto scales = [&](int (&e)[BL]) {
+#pragma unroll
+        for (int k = 0; k < BL; ++k) {
+            ks[k] = vs[k] = 1u;
+            if (e[k] < 0 || e[k] >= d.num_blocks) {
+                atomicOr(d.ws + kWsErr, kErrBadBlock);
+                e[k] = int(d.num_blocks);  // past the tensor's end: zeros
+            } else if (FP8) {
+                const int64_t at = int64_t(e[k]) * d.Hkv + part.h;
+                ks[k] = __ldg(p.k_scale + at);
+                vs[k] = __ldg(p.v_scale + at);
+            }
+        }
+    };
+    entries(lane, id);
+    entries(lane + T, id2);
+    scales(id);
+    const int depth = d.nst / T;  // turns in the ring
+    int slot = 0;                 // of this turn
+    uint32_t phase = 0;
+    bool ok = true;
+    int turn = 0;
+    for (int i = lane; i - lane < n; i += T, ++turn) {
+        const bool mine = works && i < n;
+        const int st = slot * T + lane;
+        if (mine && turn >= depth)
+            ok = mbar_wait(smem_u32(&ring.empty[st]), phase ^ 1u, kWaitLimitNs);
+        if (!__all_sync(kFull, ok)) {
+            ok = false;
+            break;
+        }
+        if (mine) {
+            const uint32_t bar = smem_u32(&ring.full[st]);
+            const int b = top - BL * i, nb = b - part.sp.b0 + 1 < BL ? b - part.sp.b0 + 1 : BL;
+            uint4 *h = reinterpret_cast<uint4 *>(&ring.hdr[st]);
+            h[0] = make_uint4(part.s, b, part.sp.T, part.h);
+            h[1] = make_uint4((turn == 0 ? F_FIRST : 0) | (i + T >= n ? F_LAST : 0), 0, 0, nb);
+            if constexpr (FP8) {
+                h[2] = make_uint4(ks[0], 0, ks[BL - 1], 0);
+                h[3] = make_uint4(vs[0], 0, vs[BL - 1], 0);
+            }
+            mbar_arrive_expect_tx(bar, uint32_t(nb) * bytes);
+            uint32_t dst = smem_u32(ring.stages) + uint32_t(st) * uint32_t(d.stage_bytes);
+#pragma unroll
+            for (int k = 0; k < BL; ++k, dst += bytes)
+                if (k < nb) {
+                    tma_load_5d_hint(dst, kmap, bar, 0, 0, 0, part.h, id[k], policy);
+                    tma_load_5d_hint(dst + bytes / 2, vmap, bar, 0, 0, 0, part.h, id[k], policy);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < BL; ++k)
+            id[k] = id2[k];
+        entries(i + 2 * T, id2);
+        scales(id);
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    if (!ok && works) {
+        if (lane == 0)
+            atomicOr(d.ws + kWsErr, kErrProducerWait);
+        // wait (bounded) for every copy that may still be in flight: the lane's stages of the
+        // last `depth` turns
+        for (int k = 0; k < depth && k < turn; ++k) {
+            if (slot == 0) {
+                slot = depth;
+                phase ^= 1u;
+            }
+            --slot;
+            if (lane + (turn - 1 - k) * T < n &&
+                !mbar_wait(smem_u32(&ring.full[slot * T + lane]), phase, kWaitLimitNs))
+                atomicOr(d.ws + kWsErr, kErrDrainWait);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ consumers
 __device__ __forceinline__ float rcp(float x)
 {
@@ -418,6 +546,18 @@ __device__ __forceinline__ void clear_empty(const ScoredParams &p, int cell, int
     }
 }
 
+// Partials of the joined form: (m, l) and output sums of row r of team t at t rows_pad + r.
+struct Partials {
+    float2 *ml;
+    float *acc;
+    // floats of a row: four more than the head, so that a warp's stores meet no bank twice
+    template <int D>
+    static __device__ __forceinline__ constexpr int stride()
+    {
+        return D + 4;
+    }
+};
+
 // The rows of a warp: NT n-tiles of 8, a lane holding rows 2 tq and 2 tq + 1 of each,
 // tokens g and g + 8 of each of up to BL blocks.
 // Above 16 rows a head takes several warps (WPH) of 16 rows. Those wait for their own
@@ -426,15 +566,16 @@ __device__ __forceinline__ void clear_empty(const ScoredParams &p, int cell, int
 // warp and a cell each. The registers for that come from the producers (setmaxnreg) and
 // from the queries, which a warp keeps in shared memory.
 constexpr __host__ __device__ bool teams_of(int wph) { return wph > 1; }
-constexpr int kTeamWarps = 12, kMaxTeams = 4;
+constexpr int kTeamWarps = 12, kMaxTeams = 4, kMaxCluster = 8;
 constexpr int kTeamThreads = 32 * (kTeamWarps + kMaxTeams);
 constexpr int kLaunchRegs = 128, kConsumerRegs = 144, kProducerRegs = 80;
 static_assert(kTeamWarps * kConsumerRegs + kMaxTeams * kProducerRegs <=
                   (kTeamWarps + kMaxTeams) * kLaunchRegs,
               "a block shares out the registers that it was launched with");
 
-template <int D, bool FP8, int NT, int WPH>
-__device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane, uint8_t *qs)
+template <int D, bool FP8, int NT, int WPH, bool JOIN>
+__device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int lane, uint8_t *qs,
+                         int team, const Partials &joins)
 {
     constexpr bool QS = teams_of(WPH);  // queries in shared memory
     constexpr int RL = 2 * NT;       // rows of a lane
@@ -471,6 +612,8 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         mul[i] = p.mul;
     }
     Turn turn;
+    if (JOIN)
+        turn.st = uint32_t(team);
     for (;;) {
         if (!mbar_wait(smem_u32(&ring.full[turn.st]), turn.phase, kWaitLimitNs)) {
             if (lane == 0)
@@ -829,9 +972,46 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_u32(&ring.empty[turn.st]));
-        turn.next(d.nst);
+        if (JOIN) {  // every p.teams'th stage (there are as many at least)
+            turn.st += uint32_t(p.teams);
+            if (turn.st >= uint32_t(d.nst)) {
+                turn.st -= uint32_t(d.nst);
+                turn.phase ^= 1u;
+            }
+        } else {
+            turn.next(d.nst);
+        }
 
-        if (flags & F_LAST) {
+        if (JOIN && (flags & F_LAST)) {
+            // ---- the team's end: its partial, for the join
+            const float vf = FP8 ? ldexpf(1.f, e_max - 127 - kWeightBits) : 1.f;
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                float l = l_r[i];
+                l += __shfl_xor_sync(kFull, l, 4);
+                l += __shfl_xor_sync(kFull, l, 8);
+                l += __shfl_xor_sync(kFull, l, 16);
+                const int row = team * d.rows_pad + row_of(i);
+                if (g == 0)
+                    joins.ml[row] = make_float2(m_r[i], l);
+                float *o = joins.acc + row * Partials::stride<D>();
+#pragma unroll
+                for (int mt = 0; mt < MT; mt += FP8 ? 2 : 1)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float v0 = acc[mt][i >> 1][2 * c + (i & 1)] * vf;
+                        if constexpr (FP8) {
+                            const float v1 = acc[mt + 1][i >> 1][2 * c + (i & 1)] * vf;
+                            *reinterpret_cast<float2 *>(o + 16 * mt + 16 * c + 2 * g) =
+                                make_float2(v0, v1);
+                        } else {
+                            o[16 * mt + 8 * c + g] = v0;
+                        }
+                    }
+            }
+            return;
+        }
+        if (!JOIN && (flags & F_LAST)) {
             // ---- the segment's end: full row sums, then the output or a partial
             const bool direct = flags & F_DIRECT;
             const float vf = FP8 ? ldexpf(1.f, e_max - 127 - kWeightBits) : 1.f;
@@ -895,7 +1075,7 @@ __global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumer
     // consumer warps of a team lie together; producers behind all of them
     const bool produces = warp >= (TEAMS ? kTeamWarps : p.d.ncw);
     const int team = !TEAMS ? 0 : produces ? warp - kTeamWarps : warp / p.d.ncw;
-    const Ring ring = carve(smem_raw, p, team);
+    const Ring ring = carve(smem_raw, p, p.teams, team);
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
@@ -921,10 +1101,169 @@ __global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumer
             const int cw = TEAMS ? warp - team * p.d.ncw : warp;
             if (p.whole)
                 clear_empty<D>(p, ring.cell, cw * 32 + lane, 32 * p.d.ncw);
-            consumer<D, FP8, NT, WPH>(p, ring, cw, lane,
-                                      query_fragments(smem_raw, p) + warp * (NT * D * 16));
+            consumer<D, FP8, NT, WPH, false>(
+                p, ring, cw, lane, query_fragments(smem_raw, p, p.teams) + warp * (NT * D * 16), 0,
+                Partials{});
         }
     }
+}
+
+// The joined form, for few and short sequences: a cluster of CTAs has one sequence and kv
+// head, a CTA an equal share of its blocks, and the teams of a CTA (a warp each up to 16
+// rows) take the stages of one ring in turn, each with a state of its own. The teams'
+// states are joined in shared memory, the CTAs' through the cluster's shared memory.
+constexpr int kJoinThreads = 256;  // seven consumer warps at most, one producer
+
+__device__ __forceinline__ uint32_t in_rank(uint32_t addr, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 cluster_f2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float4 cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+// Adds one of n partials (m, l, a) to (M, L, A), M the largest m of all. One without a
+// weight (a row that sees none of its tokens) leaves nothing to add.
+__device__ __forceinline__ void add_partial(float M, float2 ml, float4 a, float &L, float4 &A)
+{
+    if (ml.y == 0.f)
+        return;
+    const float w = ml.x == M ? 1.f : ex2(ml.x - M);
+    L = fmaf(w, ml.y, L);
+    A.x = fmaf(w, a.x, A.x);
+    A.y = fmaf(w, a.y, A.y);
+    A.z = fmaf(w, a.z, A.z);
+    A.w = fmaf(w, a.w, A.w);
+}
+
+template <int D, bool FP8, int NT, int WPH>
+__global__ void __launch_bounds__(kJoinThreads, NT == 1 ? 2 : 1)
+    scored_join_kernel(const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ ScoredParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const DecodeParams &d = p.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = p.teams * WPH;
+    const Ring ring = carve(smem_raw, p, 1, 0);
+    uint8_t *qs = query_fragments(smem_raw, p, 1);
+    Partials joins;
+    joins.acc = reinterpret_cast<float *>(qs + (teams_of(WPH) ? n_warps * NT * D * 16 : 0));
+    joins.ml = reinterpret_cast<float2 *>(joins.acc +
+                                          p.teams * d.rows_pad * Partials::stride<D>());
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        for (int i = 0; i < d.nst; ++i) {
+            mbar_init(smem_u32(&ring.full[i]), 1);
+            mbar_init(smem_u32(&ring.empty[i]), WPH);
+        }
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < p.teams * d.rows_pad; i += kJoinThreads)
+        joins.ml[i] = make_float2(-INFINITY, 0.f);
+    // the kernel before this one on the stream may still write q or the pools
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    const Share part = share<FP8>(p);
+    if (warp == n_warps) {
+        produce_share<FP8>(&kmap, &vmap, p, ring, part, lane);
+    } else if (warp < n_warps) {
+        const int team = warp / WPH;
+        if (team < part.hi - part.lo)
+            consumer<D, FP8, NT, WPH, true>(p, ring, warp % WPH, lane, qs + warp * (NT * D * 16),
+                                            team, joins);
+    }
+    __syncthreads();
+
+    // ---- the teams' partials: one for the CTA (the teams' first), or the output
+    constexpr int DQ = D / 4;
+    const auto put = [&](int row, int c, float L, float4 A) {
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
+        const int j = row / d.G;
+        const int64_t o = ((int64_t(part.s) * d.nq + j) * d.Hq + int64_t(part.h) * d.G + row -
+                           j * d.G) * D + 4 * c;
+        if (d.out_f32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(d.out) + o) = A;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(d.out) + o) =
+                make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
+    };
+    for (int i0 = 0; i0 < d.rows * DQ; i0 += kJoinThreads) {
+        const int i = i0 + threadIdx.x, row = i / DQ, c = i % DQ;
+        float M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < d.rows) {
+            for (int t = 0; t < p.teams; ++t)
+                M = fmaxf(M, joins.ml[t * d.rows_pad + row].x);
+            for (int t = 0; t < p.teams; ++t) {
+                const int r = t * d.rows_pad + row;
+                add_partial(M, joins.ml[r],
+                            *reinterpret_cast<const float4 *>(joins.acc +
+                                                              r * Partials::stride<D>() + 4 * c),
+                            L, A);
+            }
+            if (p.cluster == 1)
+                put(row, c, L, A);
+        }
+        if (p.cluster > 1) {
+            __syncthreads();  // (all of a row have read its (m, l); 256 threads have whole rows)
+            if (row < d.rows) {
+                *reinterpret_cast<float4 *>(joins.acc + row * Partials::stride<D>() + 4 * c) = A;
+                if (c == 0)
+                    joins.ml[row] = make_float2(M, L);
+            }
+        }
+    }
+    if (p.cluster == 1)
+        return;
+
+    // ---- the CTAs' partials: each CTA joins and writes a part of the rows' elements
+    cluster_barrier();
+    const int n = d.rows * DQ, hi = int(int64_t(n) * (part.rank + 1) / p.cluster);
+    for (int i = int(int64_t(n) * part.rank / p.cluster) + threadIdx.x; i < hi; i += kJoinThreads) {
+        const int row = i / DQ, c = i % DQ;
+        const uint32_t ml = smem_u32(joins.ml + row);
+        const uint32_t acc = smem_u32(joins.acc + row * Partials::stride<D>() + 4 * c);
+        float2 m[kMaxCluster];
+        float4 a[kMaxCluster];
+        float M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < p.cluster) {
+                m[r] = cluster_f2(in_rank(ml, r));
+                a[r] = cluster_f4(in_rank(acc, r));
+            }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < p.cluster)
+                M = fmaxf(M, m[r].x);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < p.cluster)
+                add_partial(M, m[r], a[r], L, A);
+        put(row, c, L, A);
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -933,9 +1272,9 @@ template <int D, bool FP8, int NT, int WPH>
 cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtensorMap &kmap,
                        const CUtensorMap &vmap, cudaStream_t stream)
 {
-    const auto kern = scored_kernel<D, FP8, NT, WPH>;
+    const auto kern = pl.cluster ? scored_join_kernel<D, FP8, NT, WPH> : scored_kernel<D, FP8, NT, WPH>;
     cudaError_t e;
-    if (teams_of(WPH)) {
+    if (teams_of(WPH) && !pl.cluster) {
         // the warps share out kLaunchRegs a thread: with fewer they would wait forever
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess)
@@ -952,18 +1291,70 @@ cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtens
     cfg.blockDim = dim3(unsigned(pl.threads));
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(pl.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pl.cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
     if (e != cudaSuccess)
         return e;
-    return pl.whole ? cudaGetLastError() : launch_merge(pl, p.d, stream);
+    return pl.whole || pl.cluster ? cudaGetLastError() : launch_merge(pl, p.d, stream);
 }
 
 }  // namespace
+
+// The joined form of a plan, where it is the faster one: it saves the second launch, the
+// walk over all sequences and the partials' way through memory, but its work is balanced
+// only inside a sequence and its CTAs stream no faster than their few warps compute. GB300,
+// E4M3, 8 kv heads, 4 rows, equal lengths, launch included, joined / cells in us:
+//   1 sequence of 333, 1000, 4000, 8000 tokens   15.2/19.1  15.3/22.6  18.8/31.6  21.7/33.8
+//   4                 1000, 4000, 8000           17.1/22.7  21.6/28.9  29.5/34.1
+//   16 (1 CTA each)   1000, 2000, 4000, 8000     22.2/28.2  27.2/33.3  42.0/42.6  69.6/64.1
+//   32 (2 on an SM)   333, 1000, 2000, 4000      19.0/26.1  29.2/33.9  45.0/44.0  75.4/63.5
+// So with one CTA on an SM up to half of the blocks a team at which both take as long (a
+// batch may hold one long sequence among short ones); with two up to 9: bf16 pools, 32
+// sequences of 2048 to 32768 tokens with a window of 1024 (66 blocks on 7 teams) take
+// 31.5/30.0.
+static bool plan_joined(int S, int Hkv, int MB, int num_sms, int smem_optin, ScoredPlan *pl)
+{
+    ScoredPlan P = *pl;
+    const int BL = stage_blocks(P.kv8);
+    const int64_t pairs = int64_t(S) * Hkv;  // of a sequence and a kv head
+    P.n_hg = Hkv;
+    P.teams = (kJoinThreads / 32 - 1) / P.wph;
+    P.threads = kJoinThreads;
+    P.stage_bytes = BL * 2 * (P.kv8 ? 1 : P.D / 64) * kTileBytes;
+    // two CTAs share an SM where one each would not do (up to 8 rows: registers)
+    P.ctas_per_sm = pairs <= num_sms ? 1 : 2;
+    if (pairs > int64_t(P.ntw == 1 ? 2 : 1) * num_sms)
+        return false;
+    // as many CTAs a pair as have work and fit (an eighth of a chip's part may be left over by
+    // clusters of eight: 16 of them took two rounds, 8 did not)
+    P.cluster = 1;
+    while (P.cluster < kMaxCluster && MB > P.cluster * P.teams * BL &&
+           pairs * P.cluster * 2 <= (P.cluster == 4 ? num_sms * 5 / 8 : num_sms))
+        P.cluster *= 2;
+    if (MB > P.cluster * P.teams * (P.ctas_per_sm == 1 ? 16 : 9))
+        return false;
+    P.grid = P.ctas = int(pairs) * P.cluster;
+    const int extra = P.teams * (P.rows_pad * ((P.D + 4) * 4 + 8) +
+                                 (teams_of(P.wph) ? P.wph * P.ntw * P.D * 16 : 0));
+    const int per_stage = P.stage_bytes + int(sizeof(Header)) + 16;
+    const int budget = P.ctas_per_sm == 1 ? smem_optin : (smem_optin + 1024) / 2 - 1024;
+    // whole turns of the teams, so that a stage is always the same team's: another team that
+    // is a turn ahead would take an old phase of its barrier for the new one
+    P.nst = std::min(2, (budget - 1024 - extra) / per_stage / P.teams) * P.teams;
+    if (P.nst < P.teams)
+        return false;
+    P.smem = 1024 + size_t(P.nst) * per_stage + extra;
+    P.ws_bytes = kWsHeaderBytes;
+    *pl = P;
+    return true;
+}
 
 int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int smem_optin,
                 int fp8, ScoredPlan *pl)
@@ -978,8 +1369,12 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     P.ntw = tiles == 1 ? 1 : 2;
     P.wph = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
     P.rows_pad = P.wph * P.ntw * 8;
-    const bool teams = teams_of(P.wph);
     P.HG = 1;
+    if (plan_joined(S, Hkv, MB, num_sms, smem_optin, &P)) {
+        *pl = P;
+        return 0;
+    }
+    const bool teams = teams_of(P.wph);
     for (int h = std::min((teams ? kTeamWarps / 3 : kConsumers) / P.wph, Hkv); h >= 1; --h)
         if (Hkv % h == 0) {
             P.HG = h;

@@ -45,7 +45,8 @@ struct ScoredParams {
     float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
     int whole;               // 1: cell c is sequence c % S of head group c / S
-    int teams, cells;        // as in the plan
+    int teams, cells;        // as in the plan (cells: its grid)
+    int cluster;             // as in the plan
     int scale_vec;           // the scale bytes of a block's 2, 4 or 8 heads are one aligned word
 };
 
@@ -53,6 +54,7 @@ struct ScoredPlan : DecodePlan {  // (grid: the cells of the call)
     int whole;  // every cell is a sequence of a head group: no pieces, no merge
     int teams;  // cells that a CTA works on at a time, each with warps and a ring of its own
     int ctas;   // of the launch
+    int cluster;  // joined form: CTAs of a sequence and kv head (0: not that form)
 };
 
 // The plan of a scored call (fp8: block-scaled pools), MB the most blocks that a
