@@ -1108,6 +1108,138 @@ __global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumer
     }
 }
 
+// Adds one of n partials (m, l, a) to (M, L, A), M the largest m of all. One without a
+// weight (a row that sees none of its tokens) leaves nothing to add.
+__device__ __forceinline__ void add_partial(float M, float2 ml, float4 a, float &L, float4 &A)
+{
+    if (ml.y == 0.f)
+        return;
+    const float w = ml.x == M ? 1.f : ex2(ml.x - M);
+    L = fmaf(w, ml.y, L);
+    A.x = fmaf(w, a.x, A.x);
+    A.y = fmaf(w, a.y, A.y);
+    A.z = fmaf(w, a.z, A.z);
+    A.w = fmaf(w, a.w, A.w);
+}
+
+// Elements 4c .. 4c + 3 of an output row: the sums A over L (zeros where nothing was seen).
+template <int D>
+__device__ __forceinline__ void write_row(const ScoredParams &p, int s, int kvh, int row, int c,
+                                          float L, float4 A)
+{
+    const DecodeParams &d = p.d;
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
+    const int j = row / d.G;
+    const int64_t o = ((int64_t(s) * d.nq + j) * d.Hq + int64_t(kvh) * d.G + row - j * d.G) * D +
+                      4 * c;
+    if (d.out_f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(d.out) + o) = A;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(d.out) + o) =
+            make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the partials of few sequences of many pieces (launch_merge has the other cases): a
+// CTA has one row, its warps an equal share of the pieces each.
+template <int D>
+__global__ void __launch_bounds__(256)
+    scored_merge_kernel(const __grid_constant__ ScoredParams p)
+{
+    __shared__ float4 s_acc[8][32];
+    __shared__ float2 s_ml[8];
+    const DecodeParams &d = p.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = d.HG * d.rows;  // of a sequence and head group
+    const int pair = int(blockIdx.x) / rows, r = int(blockIdx.x) - pair * rows;
+    const int s = pair / d.n_hg, hg = pair - s * d.n_hg;
+    const int hl = r / d.rows, row = r - hl * d.rows;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (span(p, s).nb == 0) {
+        if (threadIdx.x * 4 < D)
+            write_row<D>(p, s, hg * d.HG + hl, row, threadIdx.x, 0.f,
+                         make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+    }
+    // the pieces kb .. ke of the sequence; one piece: finished in place. (A record that is none
+    // of this call's, after a main kernel that gave up, names no cells: nothing to join.)
+    const int2 rec = __ldcg(d.pieces + int64_t(s) * d.n_hg + hg);
+    const int kb = rec.x >> 1, ke = rec.y;
+    if (kb < 0 || ke <= kb || ke >= p.cells)
+        return;
+    Cells C{};
+    const bool dense = __ldcg(d.ws + kWsDense) != 0u;
+    if (!dense) {  // fewer units than cells: some cells are empty and hold nothing
+        C.F = C.F1 = int64_t(d.n_hg) * int64_t(__ldcg(d.ws + kWsUnits));
+        C.G = p.cells;
+    }
+    const int np = ke - kb + 1, n0 = np * warp / 8, n1 = np * (warp + 1) / 8;
+    float M = -INFINITY, L = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = n0; k0 < n1; k0 += 32) {
+        const int n = n1 - k0 < 32 ? n1 - k0 : 32;
+        const int64_t cell = int64_t(kb) + k0 + lane;
+        int64_t at = -1;  // the lane's partial row
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n && (dense || !C.empty(cell))) {
+            at = (cell * 2 + (k0 + lane == 0 ? (rec.x & 1) : 0)) * rows + r;
+            ml = __ldcg(reinterpret_cast<const float2 *>(d.ml) + at);
+        }
+        float m = ml.x;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        m = fmaxf(m, M);
+        const float f = M == m ? 1.f : ex2(M - m);
+        // (a piece without a weight leaves nothing to add)
+        const float w = ml.y == 0.f ? 0.f : ml.x == m ? 1.f : ex2(ml.x - m);
+        float l = ml.y == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            l += __shfl_xor_sync(kFull, l, o);
+        M = m;
+        L = fmaf(L, f, l);
+        A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
+        constexpr int PB = 8;  // pieces on their way at a time
+        for (int j = 0; j < n; j += PB) {
+            float4 v[PB];
+            float wj[PB];
+#pragma unroll
+            for (int k = 0; k < PB; ++k) {
+                const int src = j + k < n ? j + k : j;
+                const int64_t from = __shfl_sync(kFull, at, src);
+                wj[k] = __shfl_sync(kFull, w, src);
+                if (j + k >= n)
+                    wj[k] = 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wj[k] != 0.f && lane * 4 < D)
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(d.part + from * D + lane * 4));
+            }
+#pragma unroll
+            for (int k = 0; k < PB; ++k) {
+                A.x = fmaf(wj[k], v[k].x, A.x);
+                A.y = fmaf(wj[k], v[k].y, A.y);
+                A.z = fmaf(wj[k], v[k].z, A.z);
+                A.w = fmaf(wj[k], v[k].w, A.w);
+            }
+        }
+    }
+    if (lane == 0)
+        s_ml[warp] = make_float2(M, L);
+    s_acc[warp][lane] = A;
+    __syncthreads();
+    if (warp != 0 || lane * 4 >= D)
+        return;
+    for (int k = 0; k < 8; ++k)
+        M = fmaxf(M, s_ml[k].x);
+    L = 0.f;
+    A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 8; ++k)
+        add_partial(M, s_ml[k], s_acc[k][lane], L, A);
+    write_row<D>(p, s, hg * d.HG + hl, row, lane, L, A);
+}
+
 // The joined form, for few and short sequences: a cluster of CTAs has one sequence and kv
 // head, a CTA an equal share of its blocks, and the teams of a CTA (a warp each up to 16
 // rows) take the stages of one ring in turn, each with a state of its own. The teams'
@@ -1137,20 +1269,6 @@ __device__ __forceinline__ float4 cluster_f4(uint32_t addr)
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-
-// Adds one of n partials (m, l, a) to (M, L, A), M the largest m of all. One without a
-// weight (a row that sees none of its tokens) leaves nothing to add.
-__device__ __forceinline__ void add_partial(float M, float2 ml, float4 a, float &L, float4 &A)
-{
-    if (ml.y == 0.f)
-        return;
-    const float w = ml.x == M ? 1.f : ex2(ml.x - M);
-    L = fmaf(w, ml.y, L);
-    A.x = fmaf(w, a.x, A.x);
-    A.y = fmaf(w, a.y, A.y);
-    A.z = fmaf(w, a.z, A.z);
-    A.w = fmaf(w, a.w, A.w);
 }
 
 template <int D, bool FP8, int NT, int WPH>
@@ -1195,18 +1313,6 @@ __global__ void __launch_bounds__(kJoinThreads, NT == 1 ? 2 : 1)
 
     // ---- the teams' partials: one for the CTA (the teams' first), or the output
     constexpr int DQ = D / 4;
-    const auto put = [&](int row, int c, float L, float4 A) {
-        const float f = L == 0.f ? 0.f : 1.f / L;
-        A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
-        const int j = row / d.G;
-        const int64_t o = ((int64_t(part.s) * d.nq + j) * d.Hq + int64_t(part.h) * d.G + row -
-                           j * d.G) * D + 4 * c;
-        if (d.out_f32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(d.out) + o) = A;
-        else
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(d.out) + o) =
-                make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
-    };
     for (int i0 = 0; i0 < d.rows * DQ; i0 += kJoinThreads) {
         const int i = i0 + threadIdx.x, row = i / DQ, c = i % DQ;
         float M = -INFINITY, L = 0.f;
@@ -1222,7 +1328,7 @@ __global__ void __launch_bounds__(kJoinThreads, NT == 1 ? 2 : 1)
                             L, A);
             }
             if (p.cluster == 1)
-                put(row, c, L, A);
+                write_row<D>(p, part.s, part.h, row, c, L, A);
         }
         if (p.cluster > 1) {
             __syncthreads();  // (all of a row have read its (m, l); 256 threads have whole rows)
@@ -1261,7 +1367,7 @@ __global__ void __launch_bounds__(kJoinThreads, NT == 1 ? 2 : 1)
         for (int r = 0; r < kMaxCluster; ++r)
             if (r < p.cluster)
                 add_partial(M, m[r], a[r], L, A);
-        put(row, c, L, A);
+        write_row<D>(p, part.s, part.h, row, c, L, A);
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
 }
@@ -1302,7 +1408,21 @@ cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtens
     e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
     if (e != cudaSuccess)
         return e;
-    return pl.whole || pl.cluster ? cudaGetLastError() : launch_merge(pl, p.d, stream);
+    if (pl.whole || pl.cluster)
+        return cudaGetLastError();
+    // the merge: a CTA a row where a sequence has eight pieces or more on average and the rows
+    // are few. GB300, E4M3, launches included, this / launch_merge in us: 1 sequence of 16000
+    // tokens, 5 rows a head 28.7/72.2, 5 sequences of 4000 29.3/39.5, 8 of 32768 to 131072, 4
+    // rows 196.3/198.5 (launches excluded); but 8 sequences of 4000 with 32 rows a head (2048
+    // rows in all) 52.7/47.1.
+    const int64_t pairs = int64_t(p.d.S) * p.d.n_hg, rows = pairs * p.d.HG * p.d.rows;
+    if (pairs * 8 > pl.grid || rows > 1024)
+        return launch_merge(pl, p.d, stream);
+    cfg.gridDim = dim3(unsigned(rows));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, scored_merge_kernel<D>, p);
 }
 
 }  // namespace
