@@ -1061,8 +1061,6 @@ __device__ void consumer(const ScoredParams &p, const Ring &ring, int cw, int la
 }
 
 constexpr int kConsumers = 8;
-// A CTA alone streams this much in about the time that the join of pieces takes.
-constexpr int64_t kWholeBytes = 256 * 1024;
 
 template <int D, bool FP8, int NT, int WPH>
 __global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumers + 1), 1)
@@ -1518,8 +1516,13 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     const int cap = P.ctas_per_sm * num_sms * P.teams;  // cells at most
     P.ctas = int(std::min<int64_t>(P.ctas_per_sm * num_sms, int64_t(P.n_hg) * S * MB));
     P.grid = P.ctas * P.teams;
-    // few and short sequences: one cell each, no second launch to join pieces
-    if (int64_t(P.n_hg) * S <= cap && int64_t(MB) * block_bytes <= kWholeBytes) {
+    // Short sequences that have a cell each: no walk over the batch, no pieces to join, but no
+    // balance between long and short ones either. GB300, E4M3, 8 kv heads, 4 rows, equal
+    // lengths, launches included, whole / cut in us: 40 sequences of 64, 256, 512, 1024 tokens
+    // 15.4/20.8 22.6/26.1 31.0/29.4 47.6/37.7; 150 of them (all cells) 18.2/27.2 28.9/38.6
+    // 40.2/50.5 63.9/74.7. Half of the length at which both take as long, as above.
+    const int64_t units = int64_t(P.n_hg) * S;
+    if (units <= cap && MB <= (2 * units >= cap ? 32 : 16)) {
         P.whole = 1;
         P.grid = P.n_hg * S;
         P.ctas = std::min(P.ctas_per_sm * num_sms, P.grid);
