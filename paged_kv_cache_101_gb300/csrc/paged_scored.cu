@@ -8,17 +8,28 @@
 // cap(z) = c tanh(z / c) = c (1 - 2 / (1 + 2^(2 z log2(e) / c))): one ex2 and one
 // reciprocal, absolute error 2^-22 c.
 //
-// Work. One unit is a 16-token block of a group of HG kv heads. The units of all
-// sequences (from the first block that any of the sequence's windows touches) lie
-// end to end; the persistent grid cuts them into equal cells, one per CTA. A
-// sequence inside one cell is finished in place; one cut by a cell's border leaves
-// its partial (m, l, acc) in the workspace for the merge kernel. The cells depend on
-// the sizes only, so results are deterministic.
+// Work. One unit is a 16-token block of a group of HG kv heads. Three forms, by rules on
+// the sizes that plan_scored explains:
+//  - cut: the units of all sequences (from the first block that any of the sequence's
+//    windows touches) lie end to end, and the persistent grid cuts them into equal
+//    cells. A sequence inside one cell is finished in place; one cut by a cell's border
+//    leaves its partials (m, l, acc) in the workspace for the merge kernel;
+//  - whole: a cell is a sequence of a head group;
+//  - joined: a cluster of CTAs has a sequence and a kv head (scored_join_kernel).
+// All depend on the sizes only, so results are deterministic.
 //
-// Staging. The last warp brings whole blocks of the group's heads by TMA (one box
+// Staging. A producer warp brings whole blocks of the group's heads by TMA (one box
 // for K, one for V: whole rows of the pool, contiguous where HG is all heads) into a
 // ring of shared-memory stages; the other warps consume, one kv head each (two or
 // four warps a head above 16 rows).
+//
+// Bounds. Up to 8 rows a head: HBM where the context is long, else what stands around the
+// stream (lengths, tables and first blocks, three trips to memory one after the other; the
+// merge's launch and three more): about 12 us a call. E4M3, 8 kv heads, 4 rows on one GB300:
+// 8 sequences of 32768 to 131072 tokens 196 us, 6.73 TB/s, 99% of the measured copy
+// bandwidth; 64 of 512 to 4096 46.5 us, 74%; one of 333 7.3 us (joined). bf16, capped, 64 of
+// 512 to 4096: 75.4 us, 91%. At 32 rows a head the consumers' instructions: 128 sequences of
+// 256 to 4096 tokens 116 us, 3.3 TB/s, issue slots 51%, ALU 45%, tensor pipe 38% busy.
 //
 // E4M3 pools. Codes become f16 (exact) on their way from shared memory to the tensor
 // cores. (mma.sync takes E4M3 operands too, but on sm_103a the compiler turns that
@@ -562,7 +573,8 @@ struct Partials {
 // tokens g and g + 8 of each of up to BL blocks.
 // Above 16 rows a head takes several warps (WPH) of 16 rows. Those wait for their own
 // results most of the time (with 8 warps on an SM the issue slots were 38% busy, the tensor
-// cores 26%), so an SM has twelve of them, in teams of up to four with a ring, a producer
+// cores 26%), so an SM has twelve of them (128 sequences x 4 queries: 166.6 -> 137.8 us, and
+// 116 since), in teams of up to four with a ring, a producer
 // warp and a cell each. The registers for that come from the producers (setmaxnreg) and
 // from the queries, which a warp keeps in shared memory.
 constexpr __host__ __device__ bool teams_of(int wph) { return wph > 1; }
@@ -1241,7 +1253,9 @@ __global__ void __launch_bounds__(256)
 // The joined form, for few and short sequences: a cluster of CTAs has one sequence and kv
 // head, a CTA an equal share of its blocks, and the teams of a CTA (a warp each up to 16
 // rows) take the stages of one ring in turn, each with a state of its own. The teams'
-// states are joined in shared memory, the CTAs' through the cluster's shared memory.
+// states are joined in shared memory, the CTAs' through the cluster's shared memory. Bound
+// by the chain of trips to memory (length, table entry, block) and one warp's time for a
+// stage, 1.3 us: one sequence of 333 tokens, 8 kv heads, E4M3, 7.3 us (10.4 us cut).
 constexpr int kJoinThreads = 256;  // seven consumer warps at most, one producer
 
 __device__ __forceinline__ uint32_t in_rank(uint32_t addr, int rank)
