@@ -146,7 +146,8 @@ pkv_status pkv_rope_kv_append_fp8_block(
  *   k_scale, v_scale  uint8 [num_blocks][num_kv_heads] for block-scaled E4M3
  *                     pools (head_dim 128); both NULL for bf16 pools (head_dim 64
  *                     or 128); one alone is PKV_ERR_NULL
- *   softcap           finite, >= 0; 0: no cap (PKV_ERR_RANGE otherwise)
+ *   softcap           finite, >= 0; 0: no cap (PKV_ERR_RANGE otherwise, or where
+ *                     3 scale / softcap is beyond float)
  *   alibi_slopes      device, float [num_q_heads], finite, or NULL
  *   window            >= 0; 0: no window (PKV_ERR_RANGE otherwise)
  *   workspace         >= pkv_workspace_size_scored(...) bytes, used as

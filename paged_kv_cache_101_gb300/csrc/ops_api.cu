@@ -159,7 +159,9 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
         return PKV_ERR_SHAPE;
     if (out_dtype != PKV_BF16 && out_dtype != PKV_FP32)
         return PKV_ERR_DTYPE;
-    if (!(softcap >= 0.f) || !isfinite(softcap) || window < 0)
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float mul = softcap > 0.f ? 2.f * scale * kLog2e / softcap : scale * kLog2e;
+    if (!(softcap >= 0.f) || !isfinite(softcap) || (softcap > 0.f && !isfinite(mul)) || window < 0)
         return PKV_ERR_RANGE;
     if (num_seqs == 0)
         return PKV_OK;
@@ -189,7 +191,7 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
                    : max_blocks_per_seq;
     if (pkv::plan_scored(num_seqs, nq, Hq, Hkv, D, most_blocks, dev.sms, dev.smem, fp8, &pl) != 0)
         return PKV_ERR_UNSUPPORTED;
-    if (workspace_bytes < pl.ws_bytes)
+    if (workspace_bytes < pkv_workspace_size_scored(num_seqs, nq, Hq, Hkv, D))
         return PKV_ERR_WORKSPACE;
     CUtensorMap kmap, vmap;
     if (!encode_pool(&kmap, k_cache, num_blocks, Hkv, D, pl.HG, fp8) ||
@@ -226,8 +228,7 @@ pkv_status scored_attention(const void *q, const void *k_cache, const void *v_ca
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.slopes = slopes;
-    constexpr float kLog2e = 1.4426950408889634f;
-    p.mul = softcap > 0.f ? 2.f * scale * kLog2e / softcap : scale * kLog2e;
+    p.mul = mul;
     p.cap_log2 = softcap * kLog2e;
     p.window = window;
     p.whole = pl.whole;

@@ -1528,14 +1528,14 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
         return -1;
     P.smem = 1024 + size_t(P.teams) * P.nst * per_stage + queries;
     const int cap = P.ctas_per_sm * num_sms * P.teams;  // cells at most
-    P.ctas = int(std::min<int64_t>(P.ctas_per_sm * num_sms, int64_t(P.n_hg) * S * MB));
+    const int64_t units = int64_t(P.n_hg) * S;
+    P.ctas = int(std::min<int64_t>(P.ctas_per_sm * num_sms, std::min<int64_t>(units, cap) * MB));
     P.grid = P.ctas * P.teams;
     // Short sequences that have a cell each: no walk over the batch, no pieces to join, but no
     // balance between long and short ones either. GB300, E4M3, 8 kv heads, 4 rows, equal
     // lengths, launches included, whole / cut in us: 40 sequences of 64, 256, 512, 1024 tokens
     // 15.4/20.8 22.6/26.1 31.0/29.4 47.6/37.7; 150 of them (all cells) 18.2/27.2 28.9/38.6
     // 40.2/50.5 63.9/74.7. Half of the length at which both take as long, as above.
-    const int64_t units = int64_t(P.n_hg) * S;
     if (units <= cap && MB <= (2 * units >= cap ? 32 : 16)) {
         P.whole = 1;
         P.grid = P.n_hg * S;

@@ -126,3 +126,41 @@ def test_captured_beside_eager_calls(mb):
     torch.cuda.synchronize()
     for w, o, a in zip(want, outs, again):
         assert torch.equal(w, o) and torch.equal(w, a)
+
+
+@pytest.mark.parametrize("mb", [None, WIDE])
+@pytest.mark.parametrize("nq,G", [(1, 4), (4, 8)])
+def test_a_small_workspace_is_refused_in_every_form(nq, G, mb):
+    b = Batch([300, 40], nq, G, 4, 128, True, mb=mb)
+    size = pkv.workspace_size_scored(2, nq, 4 * G, 4, 128)
+    b.check(b.call(ws=torch.zeros(size, dtype=torch.uint8, device="cuda")))
+    with pytest.raises(pkv.PkvError):
+        b.call(ws=torch.zeros(size - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("nq,G", [(1, 4), (4, 8)])
+def test_short_sequences_with_a_cell_each(nq, G):
+    """More pairs of a sequence and a head than clusters take, up to 32 blocks, none and one."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 500, 80)
+    lens[:3] = 0, 1, 512
+    b = Batch(lens, nq, G, 8, 128, True)
+    b.check(b.call())
+    sl = slopes_of(b.Hq)
+    b.check(b.call(torch.bfloat16, softcap=20.0, slopes=sl), 20.0, sl)
+    bb = Batch(lens, nq, G, 8, 64, False)
+    bb.check(bb.call())
+
+
+def test_rows_behind_the_batch_stay():
+    """Nothing is written behind the last row, in any form."""
+    for mb in (None, WIDE):
+        for lens in ([700, 33], [900] * 3, list(range(0, 400, 5))):
+            b = Batch(lens, 1, 4, 8, 128, True, mb=mb)
+            q, kc, vc, bt, cl, ks, vs = b.device()
+            n = q.shape[0]
+            out = torch.full((n + 8,) + tuple(q.shape[1:]), 7.0, dtype=torch.float32, device="cuda")
+            pkv.paged_decode_attention_fp8_block(q, kc, vc, ks, vs, bt, cl, 1, b.scale, out[:n])
+            torch.cuda.synchronize()
+            assert (out[n:] == 7.0).all()
+            b.check(out[:n])

@@ -152,6 +152,11 @@ def test_attention_refusals(lib):
         assert att(lib, **o) == ALIGN, o
 
 
+def test_caps_that_leave_float_are_refused(lib):
+    assert att(lib, cap=1e-40) == RANGE and att(lib, cap=1e-10, scale=1e35) == RANGE
+    assert att(lib, cap=1e-40, scale=1e-5, S=0) == OK
+
+
 def test_fp8_block_refusals(lib):
     def go(**over):
         a = dict(ATT, ks=A, vs=A)
