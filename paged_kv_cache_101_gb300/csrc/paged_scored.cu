@@ -14,7 +14,7 @@
 //    windows touches) lie end to end, and the persistent grid cuts them into equal
 //    cells. A sequence inside one cell is finished in place; one cut by a cell's border
 //    leaves its partials (m, l, acc) in the workspace for the merge kernel;
-//  - whole: a cell is a sequence of a head group;
+//  - whole: a cell is a sequence of a head group, or as many as an equal share comes to;
 //  - joined: a cluster of CTAs has a sequence and a kv head (scored_join_kernel).
 // All depend on the sizes only, so results are deterministic.
 //
@@ -257,7 +257,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
     const DecodeParams &d = p.d;
     const int S = d.S;
     int64_t total = 0;
-    if (!p.whole) {
+    if (p.whole != kOwnCells) {
 #pragma unroll 8
         for (int s = lane; s < S; s += 32)
             total += span(p, s).nb;
@@ -275,7 +275,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
         d.ws[kWsDense] = C.F >= C.G ? 1u : 0u;
     }
     int64_t a, e;
-    if (p.whole) {
+    if (p.whole == kOwnCells) {
         a = 0;
         e = ring.cell < p.cells ? span(p, ring.cell % S).nb : 0;
     } else {
@@ -298,7 +298,7 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
 
     if (a < e) {
         int hg, s = 0, b = 0;
-        if (p.whole) {
+        if (p.whole == kOwnCells) {
             hg = ring.cell / S;
             s = ring.cell - hg * S;
         } else {
@@ -325,6 +325,27 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
             }
         }
         Span sp = span(p, s);
+        const auto next_sequence = [&] {
+            do {
+                if (++s == S) {
+                    s = 0;
+                    ++hg;
+                }
+                sp = span(p, s);
+            } while (sp.nb == 0);
+        };
+        // borders inside a sequence move to its start or, from the middle on, to its end
+        const auto end_at_border = [&](int64_t u) {
+            if (p.whole == kRoundedCells && u < e && u + sp.nb > e)
+                e = 2 * (e - u) >= sp.nb ? u + sp.nb : u;
+        };
+        if (p.whole == kRoundedCells && b > 0) {
+            a += 2 * b >= sp.nb ? sp.nb - b : -b;
+            if (2 * b >= sp.nb && a < e)
+                next_sequence();
+            b = 0;
+        }
+        end_at_border(a);
         b = sp.b0 + sp.nb - 1 - b;  // the newest block comes first
         const uint64_t policy = policy_evict_first();
         bool opens = true;        // no segment of this cell ended yet
@@ -392,13 +413,8 @@ __device__ void producer(const CUtensorMap *kmap, const CUtensorMap *vmap, const
             if (last)
                 opens = false;
             if (b < sp.b0 && u < e) {
-                do {
-                    if (++s == S) {
-                        s = 0;
-                        ++hg;
-                    }
-                    sp = span(p, s);
-                } while (sp.nb == 0);
+                next_sequence();
+                end_at_border(u);
                 b = sp.b0 + sp.nb - 1;
                 blk.reset();
             }
@@ -541,13 +557,13 @@ constexpr float kLead = 8.f;
 // E4M3: weights are scaled by 2^6 (at most 2^14 with the lead; f16 ends at 2^16)
 constexpr int kWeightBits = 6;
 
-// A whole-sequence cell whose sequence has no token: zeros for its heads.
+// Sequence id % S of head group id / S, where it has no token: zeros for its heads.
 template <int D>
-__device__ __forceinline__ void clear_empty(const ScoredParams &p, int cell, int tid, int threads)
+__device__ __forceinline__ void clear_empty(const ScoredParams &p, int64_t id, int tid, int threads)
 {
     const DecodeParams &d = p.d;
-    const int hg = cell / d.S, s = cell - hg * d.S;
-    if (cell >= p.cells || seq_tokens(d, s) > 0)
+    const int hg = int(id / d.S), s = int(id - int64_t(hg) * d.S);
+    if (seq_tokens(d, s) > 0)
         return;
     const int row = d.HG * d.G * D / (d.out_f32 ? 4 : 8);  // 16-byte words
     for (int e = tid; e < d.nq * row; e += threads) {
@@ -1109,8 +1125,9 @@ __global__ void __launch_bounds__(teams_of(WPH) ? kTeamThreads : 32 * (kConsumer
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
         if (team < p.teams) {
             const int cw = TEAMS ? warp - team * p.d.ncw : warp;
-            if (p.whole)
-                clear_empty<D>(p, ring.cell, cw * 32 + lane, 32 * p.d.ncw);
+            if (p.whole)  // (otherwise the merge does it)
+                for (int64_t id = ring.cell; id < int64_t(p.d.S) * p.d.n_hg; id += p.cells)
+                    clear_empty<D>(p, id, cw * 32 + lane, 32 * p.d.ncw);
             consumer<D, FP8, NT, WPH, false>(
                 p, ring, cw, lane, query_fragments(smem_raw, p, p.teams) + warp * (NT * D * 16), 0,
                 Partials{});
@@ -1537,10 +1554,19 @@ int plan_scored(int S, int nq, int Hq, int Hkv, int D, int MB, int num_sms, int 
     // 15.4/20.8 22.6/26.1 31.0/29.4 47.6/37.7; 150 of them (all cells) 18.2/27.2 28.9/38.6
     // 40.2/50.5 63.9/74.7. Half of the length at which both take as long, as above.
     if (units <= cap && MB <= (2 * units >= cap ? 32 : 16)) {
-        P.whole = 1;
+        P.whole = kOwnCells;
         P.grid = P.n_hg * S;
         P.ctas = std::min(P.ctas_per_sm * num_sms, P.grid);
     }
+    // More short sequences than cells: borders that move to the ends of sequences leave cells
+    // that differ by a sequence at most, and nothing to join. The same, rounded / cut: 160
+    // sequences (152 cells) of 64, 256, 512 tokens 24.3/26.8 39.2/37.2 59.4/50.3, of a tenth
+    // to all of that 21.2/27.4 30.2/32.5 40.5/42.9; 600 of 64, 256, 512, 1024 34.5/43.0
+    // 70.7/77.2 116/124 211/218, ragged 36.5/42.0 53.3/60.0 82.9/81.8 141/136. 32 rows a head
+    // (more to join): 130 sequences (456 cells, 520 units) of 64, 256, 512, 1024 29.3/41.2
+    // 47.0/59.7 68.8/73.5 113/102; 310 39.4/56.6 70.5/90.8 112/126 192/196.
+    if (units > cap && MB <= (teams ? 32 : units >= 3 * int64_t(cap) ? 16 : 8))
+        P.whole = kRoundedCells;
     P.off_rec = kWsHeaderBytes;
     P.off_ml = P.off_rec + round_up(size_t(S) * P.n_hg * 8, 256);
     P.off_part = P.off_ml + round_up(size_t(cap) * 2 * P.HG * P.rows * 2 * 4, 256);

@@ -36,6 +36,10 @@ cudaError_t launch_rope_append(const RopeParams &p, RopeForm form, cudaStream_t 
 
 constexpr int kMaxFp8BlockDim = 256;  // head_dim of the block-scaled append
 
+// Cells that cut no sequence: cell c is sequence c % S of head group c / S, or the borders of
+// equal cells move to the nearer end of the sequence that they fall into.
+enum { kOwnCells = 1, kRoundedCells = 2 };
+
 struct ScoredParams {
     DecodeParams d;          // the decode call's own parameters (the merge reads these)
     const uint8_t *k_scale;  // [num_blocks][Hkv] scale bytes (null: bf16 pools)
@@ -44,14 +48,14 @@ struct ScoredParams {
     float mul;               // to the log2 domain: scale log2(e), or 2 scale log2(e) / softcap
     float cap_log2;          // softcap log2(e); 0: none
     int window;              // 0: none
-    int whole;               // 1: cell c is sequence c % S of head group c / S
+    int whole;               // as in the plan
     int teams, cells;        // as in the plan (cells: its grid)
     int cluster;             // as in the plan
     int scale_vec;           // the scale bytes of a block's 2, 4 or 8 heads are one aligned word
 };
 
 struct ScoredPlan : DecodePlan {  // (grid: the cells of the call)
-    int whole;  // every cell is a sequence of a head group: no pieces, no merge
+    int whole;  // kOwnCells, kRoundedCells (no pieces, no merge) or 0
     int teams;  // cells that a CTA works on at a time, each with warps and a ring of its own
     int ctas;   // of the launch
     int cluster;  // joined form: CTAs of a sequence and kv head (0: not that form)

@@ -164,3 +164,24 @@ def test_rows_behind_the_batch_stay():
             torch.cuda.synchronize()
             assert (out[n:] == 7.0).all()
             b.check(out[:n])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,G,S,top", [(1, 4, 170, 128), (1, 2, 470, 256), (4, 8, 125, 500)])
+def test_cells_of_several_short_sequences(fp8, nq, G, S, top):
+    """More pairs of a sequence and a head group than cells; empty ones, runs of them, and
+    single long ones among tiny ones."""
+    rng = np.random.default_rng(S)
+    lens = rng.integers(0, top + 1, S)
+    lens[rng.integers(0, S, S // 5)] = 0
+    lens[:4] = 0, 0, top, 1
+    lens[-3:] = top, 0, 0
+    for ls in (lens, np.where(np.arange(S) % 40 == 7, top, np.minimum(lens, 3))):
+        b = Batch(ls, nq, G, 8, 128, fp8)
+        b.check(b.call())
+    b = Batch(np.zeros(S, int), nq, G, 8, 128, fp8)
+    assert not b.call().any()
+    one = np.zeros(S, int)
+    one[S // 2] = top
+    b = Batch(one, nq, G, 8, 128, fp8)
+    b.check(b.call())
