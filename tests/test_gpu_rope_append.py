@@ -85,6 +85,16 @@ def test_rotation_and_append(n, Hq, Hkv, D, r, interleaved):
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n,Hq,Hkv,D,r", [(1300, 1, 1, 96, 24), (2443, 3, 1, 24, 6),
+                                          (1217, 4, 2, 80, 42), (1300, 1, 1, 136, 130),
+                                          (9001, 1, 1, 24, 6), (1900, 2, 1, 1024, 1000)])
+def test_many_rows_of_odd_dims(n, Hq, Hkv, D, r, interleaved):
+    """Dims that no vector form takes, several rows to a block of threads."""
+    run(Case(n, Hq, Hkv, D, r, pad=(0, 1, n // 2, n - 1), positions=np.arange(n) * 7919 - 5),
+        interleaved)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
 def test_far_and_negative_positions(interleaved):
     pos = [0, 1, -1, 131071, 10 ** 6 + 7, 2 ** 31 - 1, 2 ** 31 + 5, -(2 ** 40) + 3, 2 ** 52 + 1,
            2 ** 63 - 1]
