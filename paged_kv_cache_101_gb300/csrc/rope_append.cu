@@ -119,18 +119,43 @@ __device__ __forceinline__ void rotate_unit(const uint16_t *src, int u, int d0, 
                 x[i + 1] = b * t.x + a * t.y;
             }
         }
-    } else {
-        const int h = p.r / 2;
+    } else if (p.interleaved) {  // (as kPairs; the rotated part may end inside a vector)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 16; i += 2) {
+            if (d0 + i < p.r) {
+                const float2 t = trig[trig_at((d0 + i) / 2, p.r / 2)];
+                const float a = x[i], b = x[i + 1];
+                x[i] = a * t.x - b * t.y;
+                x[i + 1] = b * t.x + a * t.y;
+            }
+        }
+    } else {
+        // halves of h dims: partners h dims away, in other vectors; four at a time where
+        // h allows it
+        const int h = p.r / 2;
+        const auto turn_one = [&](int i, float other) {
             const int d = d0 + i;
-            if (d < p.r) {  // r <= D: d is a dim of the head
-                const bool second = p.interleaved ? (d & 1) : d >= h;
-                const int j = p.interleaved ? d / 2 : (second ? d - h : d);
-                const int o = p.interleaved ? d ^ 1 : (second ? j : d + h);
-                const float2 t = trig[trig_at(j, h)];
-                const float other = __uint_as_float(uint32_t(src[o]) << 16);
-                x[i] = second ? x[i] * t.x + other * t.y : x[i] * t.x - other * t.y;
+            const bool second = d >= h;
+            const float2 t = trig[trig_at(second ? d - h : d, h)];
+            x[i] = second ? x[i] * t.x + other * t.y : x[i] * t.x - other * t.y;
+        };
+        if (h % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (d0 + i < p.r) {
+                    const int d = d0 + i;
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src + (d >= h ? d - h : d + h));
+                    turn_one(i, bf16lo_f32(w.x));
+                    turn_one(i + 1, bf16hi_f32(w.x));
+                    turn_one(i + 2, bf16lo_f32(w.y));
+                    turn_one(i + 3, bf16hi_f32(w.y));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int d = d0 + i;
+                if (d < p.r)  // r <= D: d is a dim of the head
+                    turn_one(i, __uint_as_float(uint32_t(src[d >= h ? d - h : d + h]) << 16));
             }
         }
     }
