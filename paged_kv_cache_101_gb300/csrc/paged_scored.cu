@@ -1168,102 +1168,82 @@ __device__ __forceinline__ void write_row(const ScoredParams &p, int s, int kvh,
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the partials of few sequences of many pieces (launch_merge has the other cases): a
-// CTA has one row, its warps an equal share of the pieces each.
-template <int D>
+// Joins the partials of few sequences of many pieces (launch_merge has the other cases): WPR
+// warps have a row, an equal share of its pieces each. Bound by three trips to memory, the
+// lengths and records, the partials, the output, of as many CTAs as are resident.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256)
     scored_merge_kernel(const __grid_constant__ ScoredParams p)
 {
     __shared__ float4 s_acc[8][32];
     __shared__ float2 s_ml[8];
     const DecodeParams &d = p.d;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
     const int rows = d.HG * d.rows;  // of a sequence and head group
-    const int pair = int(blockIdx.x) / rows, r = int(blockIdx.x) - pair * rows;
+    const int64_t id = int64_t(blockIdx.x) * (8 / WPR) + warp / WPR;
+    const int pair = int(id / rows), r = int(id - int64_t(pair) * rows);
     const int s = pair / d.n_hg, hg = pair - s * d.n_hg;
     const int hl = r / d.rows, row = r - hl * d.rows;
+    const bool here = s < d.S;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (span(p, s).nb == 0) {
-        if (threadIdx.x * 4 < D)
-            write_row<D>(p, s, hg * d.HG + hl, row, threadIdx.x, 0.f,
-                         make_float4(0.f, 0.f, 0.f, 0.f));
-        return;
-    }
     // the pieces kb .. ke of the sequence; one piece: finished in place. (A record that is none
     // of this call's, after a main kernel that gave up, names no cells: nothing to join.)
-    const int2 rec = __ldcg(d.pieces + int64_t(s) * d.n_hg + hg);
-    const int kb = rec.x >> 1, ke = rec.y;
-    if (kb < 0 || ke <= kb || ke >= p.cells)
-        return;
-    Cells C{};
+    const int2 rec = here ? __ldcg(d.pieces + int64_t(s) * d.n_hg + hg) : make_int2(0, 0);
+    const bool empty = here && span(p, s).nb == 0;
     const bool dense = __ldcg(d.ws + kWsDense) != 0u;
-    if (!dense) {  // fewer units than cells: some cells are empty and hold nothing
+    const int kb = rec.x >> 1, ke = rec.y;
+    const bool joins = here && !empty && kb >= 0 && ke > kb && ke < p.cells;
+    Cells C{};
+    if (joins && !dense) {  // fewer units than cells: some cells are empty and hold nothing
         C.F = C.F1 = int64_t(d.n_hg) * int64_t(__ldcg(d.ws + kWsUnits));
         C.G = p.cells;
     }
-    const int np = ke - kb + 1, n0 = np * warp / 8, n1 = np * (warp + 1) / 8;
+    const int np = joins ? ke - kb + 1 : 0, n1 = np * (sub + 1) / WPR;
     float M = -INFINITY, L = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = n0; k0 < n1; k0 += 32) {
-        const int n = n1 - k0 < 32 ? n1 - k0 : 32;
+    constexpr int PB = 8;  // pieces at a time
+    for (int k0 = np * sub / WPR; k0 < n1; k0 += PB) {
         const int64_t cell = int64_t(kb) + k0 + lane;
         int64_t at = -1;  // the lane's partial row
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < n && (dense || !C.empty(cell))) {
+        if (lane < PB && k0 + lane < n1 && (dense || !C.empty(cell)))
             at = (cell * 2 + (k0 + lane == 0 ? (rec.x & 1) : 0)) * rows + r;
-            ml = __ldcg(reinterpret_cast<const float2 *>(d.ml) + at);
+        const float2 ml = at >= 0 ? __ldcg(reinterpret_cast<const float2 *>(d.ml) + at)
+                                  : make_float2(-INFINITY, 0.f);
+        float4 v[PB];
+#pragma unroll
+        for (int k = 0; k < PB; ++k) {
+            const int64_t from = __shfl_sync(kFull, at, k);
+            v[k] = from >= 0 && lane * 4 < D
+                       ? __ldcg(reinterpret_cast<const float4 *>(d.part + from * D + lane * 4))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float m = ml.x;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
+        for (int o = PB / 2; o >= 1; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        m = fmaxf(m, M);
+        m = fmaxf(__shfl_sync(kFull, m, 0), M);
         const float f = M == m ? 1.f : ex2(M - m);
-        // (a piece without a weight leaves nothing to add)
-        const float w = ml.y == 0.f ? 0.f : ml.x == m ? 1.f : ex2(ml.x - m);
-        float l = ml.y == 0.f ? 0.f : w * ml.y;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            l += __shfl_xor_sync(kFull, l, o);
         M = m;
-        L = fmaf(L, f, l);
+        L *= f;
         A = make_float4(A.x * f, A.y * f, A.z * f, A.w * f);
-        constexpr int PB = 8;  // pieces on their way at a time
-        for (int j = 0; j < n; j += PB) {
-            float4 v[PB];
-            float wj[PB];
 #pragma unroll
-            for (int k = 0; k < PB; ++k) {
-                const int src = j + k < n ? j + k : j;
-                const int64_t from = __shfl_sync(kFull, at, src);
-                wj[k] = __shfl_sync(kFull, w, src);
-                if (j + k >= n)
-                    wj[k] = 0.f;
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wj[k] != 0.f && lane * 4 < D)
-                    v[k] = __ldcg(reinterpret_cast<const float4 *>(d.part + from * D + lane * 4));
-            }
-#pragma unroll
-            for (int k = 0; k < PB; ++k) {
-                A.x = fmaf(wj[k], v[k].x, A.x);
-                A.y = fmaf(wj[k], v[k].y, A.y);
-                A.z = fmaf(wj[k], v[k].z, A.z);
-                A.w = fmaf(wj[k], v[k].w, A.w);
-            }
-        }
+        for (int k = 0; k < PB; ++k)
+            add_partial(M,
+                        make_float2(__shfl_sync(kFull, ml.x, k), __shfl_sync(kFull, ml.y, k)),
+                        v[k], L, A);
     }
     if (lane == 0)
         s_ml[warp] = make_float2(M, L);
     s_acc[warp][lane] = A;
     __syncthreads();
-    if (warp != 0 || lane * 4 >= D)
+    if (sub != 0 || lane * 4 >= D || !(joins || empty))
         return;
-    for (int k = 0; k < 8; ++k)
-        M = fmaxf(M, s_ml[k].x);
+    for (int k = 0; k < WPR; ++k)
+        M = fmaxf(M, s_ml[warp + k].x);
     L = 0.f;
     A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < 8; ++k)
-        add_partial(M, s_ml[k], s_acc[k][lane], L, A);
+    for (int k = 0; k < WPR; ++k)
+        add_partial(M, s_ml[warp + k], s_acc[warp + k][lane], L, A);
     write_row<D>(p, s, hg * d.HG + hl, row, lane, L, A);
 }
 
@@ -1439,19 +1419,21 @@ cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtens
         return e;
     if (pl.whole || pl.cluster)
         return cudaGetLastError();
-    // the merge: a CTA a row where a sequence has eight pieces or more on average and the rows
-    // are few. GB300, E4M3, launches included, this / launch_merge in us: 1 sequence of 16000
-    // tokens, 5 rows a head 28.7/72.2, 5 sequences of 4000 29.3/39.5, 8 of 32768 to 131072, 4
-    // rows 196.3/198.5 (launches excluded); but 8 sequences of 4000 with 32 rows a head (2048
-    // rows in all) 52.7/47.1.
+    // The merge: eight or four warps a row where a sequence has eight pieces or more on average
+    // and the rows are few. GB300, E4M3, launches included, 8 kv heads, eight warps / four /
+    // launch_merge in us: 1 sequence of 8000 tokens with 32 rows a head (256 rows in all)
+    // 30.8/34.5/65.8, 3 with 16 (384) 34.5/36.1/53.2, 5 (640) 43.2/40.2/49.8, 8 (1024)
+    // 50.1/46.4/51.6, 5 with 32 (1280) 51.2/49.3/53.4, 8 (2048) 66.9/62.3/62.9, 16 with 16
+    // (2048) 77.3/72.1/69.8.
     const int64_t pairs = int64_t(p.d.S) * p.d.n_hg, rows = pairs * p.d.HG * p.d.rows;
-    if (pairs * 8 > pl.grid || rows > 1024)
+    if (pairs * 8 > pl.grid || rows > 1536)
         return launch_merge(pl, p.d, stream);
-    cfg.gridDim = dim3(unsigned(rows));
+    const bool all = rows <= 512;
+    cfg.gridDim = dim3(unsigned(all ? rows : (rows + 1) / 2));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_merge_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, all ? scored_merge_kernel<D, 8> : scored_merge_kernel<D, 4>, p);
 }
 
 }  // namespace
