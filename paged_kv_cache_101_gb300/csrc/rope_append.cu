@@ -248,7 +248,11 @@ template <int FORM, bool KV>
 __device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int part, int split,
                                            int lane)
 {
-    constexpr int kAhead = 3;
+    // three CTAs of an SM with 80 registers a thread, or two with 128 (the block-scaled
+    // append's own need). 8,190 rows of 64 q and 8 kv heads, block-scaled, 3 / 4 / 6 / 8 / 10
+    // heads ahead: 61.0 / 57.7 / 56.3 / 54.3 / 55.7 us; 8,190 of 32 and 8, bf16, 3 with three
+    // CTAs, 6 or 8 with two: 33.4 / 35.2 / 38.0.
+    constexpr int kAhead = KV ? 3 : 8;
     const int per = 32 / p.units;  // heads of one group
     const int u = lane % p.units, sub = lane / p.units;
     int d0, d1;
@@ -583,8 +587,7 @@ __device__ __forceinline__ void append_run_128(const RopeParams &p, const Raw (&
 // that finds none still costs its slot on an SM: 8,190 rows, K and V alone, 42.3 us with
 // eight rows looked at one after another, 24.9 us with one look at eight, 18.8 us at sixteen). Bound
 // by the latency of slots, then rows, then stores while rows are few (64 rows with q:
-// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 61.0 us, 77% of the measured copy
-// bandwidth: 46 us of it are q.
+// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 54.3 us, 86% of the measured copy bandwidth.
 // PASSES 0: heads of 128 dims in vector form.
 template <int FORM, int PASSES>
 __global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8_kernel(const RopeParams p, int split,
