@@ -1168,7 +1168,7 @@ __device__ __forceinline__ void write_row(const ScoredParams &p, int s, int kvh,
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the partials of few sequences of many pieces (launch_merge has the other cases): WPR
+// Joins the partials of few rows (launch_merge has the other cases): WPR
 // warps have a row, an equal share of its pieces each. Bound by three trips to memory, the
 // lengths and records, the partials, the output, of as many CTAs as are resident.
 template <int D, int WPR>
@@ -1201,7 +1201,7 @@ __global__ void __launch_bounds__(256)
     const int np = joins ? ke - kb + 1 : 0, n1 = np * (sub + 1) / WPR;
     float M = -INFINITY, L = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int PB = 8;  // pieces at a time
+    constexpr int PB = WPR == 1 ? 4 : 8;  // pieces at a time
     for (int k0 = np * sub / WPR; k0 < n1; k0 += PB) {
         const int64_t cell = int64_t(kb) + k0 + lane;
         int64_t at = -1;  // the lane's partial row
@@ -1419,21 +1419,26 @@ cudaError_t launch_one(const ScoredPlan &pl, const ScoredParams &p, const CUtens
         return e;
     if (pl.whole || pl.cluster)
         return cudaGetLastError();
-    // The merge: eight or four warps a row where a sequence has eight pieces or more on average
-    // and the rows are few. GB300, E4M3, launches included, 8 kv heads, eight warps / four /
-    // launch_merge in us: 1 sequence of 8000 tokens with 32 rows a head (256 rows in all)
-    // 30.8/34.5/65.8, 3 with 16 (384) 34.5/36.1/53.2, 5 (640) 43.2/40.2/49.8, 8 (1024)
+    // The merge. GB300, E4M3, 8 kv heads. Where a sequence has eight pieces or more on average,
+    // eight or four warps a row while the rows are few; eight warps / four / launch_merge,
+    // launches included, in us: 1 sequence of 8000 tokens with 32 rows a head (256 rows in
+    // all) 30.8/34.5/65.8, 3 with 16 (384) 34.5/36.1/53.2, 5 (640) 43.2/40.2/49.8, 8 (1024)
     // 50.1/46.4/51.6, 5 with 32 (1280) 51.2/49.3/53.4, 8 (2048) 66.9/62.3/62.9, 16 with 16
-    // (2048) 77.3/72.1/69.8.
+    // (2048) 77.3/72.1/69.8. With fewer pieces one warp a row while those all fit; one warp /
+    // launch_merge: 64 sequences of 512 to 4096 with 4 rows (2048) 46.2/46.9, 256 of 300 to
+    // 2500 with 8 (16384) 98.8/96.0, 128 of 256 to 4096 with 32 (32768) 121.9/116.3.
     const int64_t pairs = int64_t(p.d.S) * p.d.n_hg, rows = pairs * p.d.HG * p.d.rows;
-    if (pairs * 8 > pl.grid || rows > 1536)
+    const bool few = pairs * 8 > pl.grid;  // pieces
+    if (rows > (few ? 4096 : 1536))
         return launch_merge(pl, p.d, stream);
-    const bool all = rows <= 512;
-    cfg.gridDim = dim3(unsigned(all ? rows : (rows + 1) / 2));
+    const int warps = few ? 1 : rows <= 512 ? 8 : 4;
+    const auto merge = few ? scored_merge_kernel<D, 1>
+                           : warps == 8 ? scored_merge_kernel<D, 8> : scored_merge_kernel<D, 4>;
+    cfg.gridDim = dim3(unsigned((rows * warps + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, all ? scored_merge_kernel<D, 8> : scored_merge_kernel<D, 4>, p);
+    return cudaLaunchKernelEx(&cfg, merge, p);
 }
 
 }  // namespace
