@@ -27,8 +27,8 @@
 // stream (lengths, tables and first blocks, three trips to memory one after the other; the
 // merge's launch and three more): about 12 us a call. E4M3, 8 kv heads, 4 rows on one GB300:
 // 8 sequences of 32768 to 131072 tokens 196 us, 6.73 TB/s, 99% of the measured copy
-// bandwidth; 64 of 512 to 4096 46.5 us, 74%; one of 333 7.3 us (joined). bf16, capped, 64 of
-// 512 to 4096: 75.4 us, 91%. At 32 rows a head the consumers' instructions: 128 sequences of
+// bandwidth; 64 of 512 to 4096 46.4 us, 74%; one of 333 7.3 us (joined). bf16, capped, 64 of
+// 512 to 4096: 75.3 us, 91%. At 32 rows a head the consumers' instructions: 128 sequences of
 // 256 to 4096 tokens 116 us, 3.3 TB/s, issue slots 51%, ALU 45%, tensor pipe 38% busy.
 //
 // E4M3 pools. Codes become f16 (exact) on their way from shared memory to the tensor
