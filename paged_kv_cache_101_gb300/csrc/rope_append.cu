@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr unsigned kAll = 0xffffffffU;
 constexpr int kMaxPairs = 512;  // head_dim <= 1024
+constexpr int kSms = 152;       // what the choices by row count are made for
 
 // Launched with programmatic serialization: wait for the kernel before this one on the
 // stream, then let the one behind it start its own prologue.
@@ -244,15 +245,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(const RopePar
 // eight sines and cosines stay in registers for all heads of the row; no shared
 // memory, no barrier, kAhead heads' loads in flight a lane. KV: k and v as well (the
 // block-scaled append runs this for q alone).
-template <int FORM, bool KV>
+// kAhead: three where three CTAs share an SM (80 registers), eight beside the block-scaled
+// append, which has 128 anyway. 8,190 rows of 64 q and 8 kv heads, block-scaled, 3 / 4 / 6 / 8 /
+// 10 heads ahead: 61.0 / 57.7 / 56.3 / 54.3 / 55.7 us (53.3 with the first ones asked for before
+// the sines); 8,190 of 32 and 8, bf16, 3 with three CTAs, 6 or 8 with two: 33.4 / 35.2 / 38.0.
+template <int FORM, bool KV, int kAhead>
 __device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int part, int split,
                                            int lane)
 {
-    // three CTAs of an SM with 80 registers a thread, or two with 128 (the block-scaled
-    // append's own need). 8,190 rows of 64 q and 8 kv heads, block-scaled, 3 / 4 / 6 / 8 / 10
-    // heads ahead: 61.0 / 57.7 / 56.3 / 54.3 / 55.7 us; 8,190 of 32 and 8, bf16, 3 with three
-    // CTAs, 6 or 8 with two: 33.4 / 35.2 / 38.0.
-    constexpr int kAhead = KV ? 3 : 8;
     const int per = 32 / p.units;  // heads of one group
     const int u = lane % p.units, sub = lane / p.units;
     int d0, d1;
@@ -261,34 +261,14 @@ __device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int p
     const int64_t slot = KV ? __ldg(p.slots + i) : -1;
     const bool stored = slot >= 0 && slot < p.total_slots;
     const int64_t pos = __ldg(p.positions + i);
-    float2 t[8];
-    // pair 8 u + c is the unit's c-th in both layouts
-    const bool turns = FORM == kHalf ? u < p.r / 16 : 16 * u < p.r;
-    auto pair = [&](int c) {
-        return turns && 8 * u + c < p.r / 2 ? turn(pos, __ldg(p.turns + 8 * u + c), p.scale)
-                                            : make_float2(0.f, 0.f);
-    };
-    if (per == 4) {
-        // four lanes hold the same unit of four heads: each computes two pairs for all
-        const float2 lo = pair(sub), hi = pair(sub + 4);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float2 from = c < 4 ? lo : hi;
-            t[c].x = __shfl_sync(kAll, from.x, (c & 3) * p.units + u);
-            t[c].y = __shfl_sync(kAll, from.y, (c & 3) * p.units + u);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            t[c] = pair(c);
-    }
     // groups of q heads, then of k's and v's (of one kind each: the choice is the warp's)
     const int nq = (p.Hq + per - 1) / per, nk = KV ? (p.Hkv + per - 1) / per : 0;
     const int groups = nq + (stored ? 2 * nk : 0);
-    for (int g0 = part; g0 < groups; g0 += split * kAhead) {
-        uint4 a[kAhead], b[kAhead];
-        uint16_t *to[kAhead];
-        bool rot[kAhead];
+    const bool turns = FORM == kHalf ? u < p.r / 16 : 16 * u < p.r;
+    uint4 a[kAhead], b[kAhead];
+    uint16_t *to[kAhead];
+    bool rot[kAhead];
+    const auto load = [&](int g0) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             int group = g0 + k * split, heads = p.Hq;
@@ -314,6 +294,31 @@ __device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int p
                     b[k] = *reinterpret_cast<const uint4 *>(from + h * p.D + d1);
             }
         }
+    };
+    load(part);  // on their way while the sines are computed
+    float2 t[8];
+    // pair 8 u + c is the unit's c-th in both layouts
+    auto pair = [&](int c) {
+        return turns && 8 * u + c < p.r / 2 ? turn(pos, __ldg(p.turns + 8 * u + c), p.scale)
+                                            : make_float2(0.f, 0.f);
+    };
+    if (per == 4) {
+        // four lanes hold the same unit of four heads: each computes two pairs for all
+        const float2 lo = pair(sub), hi = pair(sub + 4);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float2 from = c < 4 ? lo : hi;
+            t[c].x = __shfl_sync(kAll, from.x, (c & 3) * p.units + u);
+            t[c].y = __shfl_sync(kAll, from.y, (c & 3) * p.units + u);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            t[c] = pair(c);
+    }
+    for (int g0 = part; g0 < groups; g0 += split * kAhead) {
+        if (g0 != part)
+            load(g0);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (!to[k])
@@ -341,14 +346,16 @@ __device__ __forceinline__ void rotate_row(const RopeParams &p, int64_t i, int p
     }
 }
 
-template <int FORM>
-__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const RopeParams p, int split)
+// FEW: CTAs that are two an SM at most, with registers to load the first heads while the
+// sines are computed: 256 rows of 64 q heads 4.5 -> 3.9 us; 320 (above it) 4.2 instead of 4.9.
+template <int FORM, bool FEW>
+__global__ void __launch_bounds__(kThreads, FEW ? 2 : 3) rope_append_kernel(const RopeParams p, int split)
 {
     begin_after_previous();
     const int warp = threadIdx.x >> 5, rows = kThreads / 32 / split;
     const int64_t i = int64_t(blockIdx.x) * rows + warp / split;
     if (i < p.n)
-        rotate_row<FORM, true>(p, i, warp % split, split, threadIdx.x & 31);
+        rotate_row<FORM, true, FEW ? 3 : 3>(p, i, warp % split, split, threadIdx.x & 31);
 }
 
 __device__ __forceinline__ uint2 encode8(const float *x, float f)
@@ -583,11 +590,11 @@ __device__ __forceinline__ void append_run_128(const RopeParams &p, const Raw (&
 // runs that start in the `window` rows from w * window on (a row starts one where the
 // row before it falls into another block), for eight heads of K (y even) or V, a warp
 // each: windows of one row while the rows are few (every token of a decode step is a
-// run of its own), of eight and sixteen above (a prompt has a run in 16 rows, and a CTA
+// run of its own), of up to sixteen above (a prompt has a run in 16 rows, and a CTA
 // that finds none still costs its slot on an SM: 8,190 rows, K and V alone, 42.3 us with
 // eight rows looked at one after another, 24.9 us with one look at eight, 18.8 us at sixteen). Bound
 // by the latency of slots, then rows, then stores while rows are few (64 rows with q:
-// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 54.3 us, 86% of the measured copy bandwidth.
+// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 53.3 us, 88% of the measured copy bandwidth.
 // PASSES 0: heads of 128 dims in vector form.
 template <int FORM, int PASSES>
 __global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8_kernel(const RopeParams p, int split,
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8
         if constexpr (FORM != kScalar) {
             const int64_t i = q_before * (kThreads / 32 / split) + warp / split;
             if (i < p.n)
-                rotate_row<FORM, false>(p, i, warp % split, split, lane);
+                rotate_row<FORM, false, 8>(p, i, warp % split, split, lane);
         } else {
             const int64_t i = q_before;
             const int64_t pos = __ldg(p.positions + i);
@@ -712,17 +719,22 @@ template <int FORM>
 cudaError_t launch(const RopeParams &p, cudaStream_t stream)
 {
     constexpr int kWarps = kThreads / 32;
-    // warps of a row: all of a CTA's while the rows are few (latency); once they fill the
-    // GPU two, and one beside the block-scaled append, whose own arithmetic fills the issue
-    // slots (each warp of a row computes its sines and cosines again). 8,190 rows, 1 / 2 / 4
-    // warps: 34.9 / 33.8 / 36.9 us in bf16 (88% of the measured copy bandwidth), 65.7 /
-    // 69.6 / 78.5 us block-scaled (an earlier form of it).
-    const int split = p.n < 1024 ? kWarps : p.k_scale ? 1 : 2;
+    // Warps of a row: as many as leave two CTAs an SM (304) or fewer, and two at least. 600 rows
+    // of 32 q and 8 kv heads, 8 / 4 / 2 warps: 5.4 / 3.6 / 3.7 us; 1000: 7.4 / - / 4.8; 8,190,
+    // 1 / 2 / 4 warps: 34.9 / 33.8 / 36.9 (33.4 now, 88% of the measured copy bandwidth). Beside
+    // the block-scaled append, whose own arithmetic fills the issue slots, one once rows are
+    // many (each warp of a row computes its sines and cosines again): 8,190 rows, 1 / 2 / 4
+    // warps: 65.7 / 69.6 / 78.5 us (an earlier form of it).
+    const int wide = p.n <= 2 * kSms ? kWarps : p.n <= 4 * kSms ? 4 : 2;
+    const int split = p.k_scale && p.n >= 1024 ? 1 : wide;
     const int rows = kWarps / split;
     const int64_t row_ctas = (p.n + rows - 1) / rows;
     if (p.k_scale) {
         const int64_t q_ctas = p.Hq == 0 ? 0 : FORM == kScalar ? p.n : row_ctas;
-        const int window = p.n < 1024 ? 1 : p.n < 4096 ? 8 : 16;
+        // (600 rows of 32 q and 8 kv heads, windows of 1 / 2 / 4 / 8: 14.2 / 13.3 / 14.6 / 18.3 us
+        // where each is a run, 10.1 / 8.4 / 6.9 / 8.1 in runs of four, 11.2 / 9.4 / 8.5 / 8.4 in
+        // one sequence; 128 rows, 1 / 2 / 4: 5.8 / 5.6 / 8.9, 4.5 / 4.0 / 3.9, 6.1 / 5.7 / 5.7)
+        const int window = p.n < 128 ? 1 : p.n < 512 ? 2 : p.n < 1024 ? 4 : p.n < 4096 ? 8 : 16;
         const int64_t grid = q_ctas + (p.n + window - 1) / window * 2 * ((p.Hkv + 7) / 8);
         if constexpr (FORM != kScalar) {
             if (p.D == 128)
@@ -737,10 +749,12 @@ cudaError_t launch(const RopeParams &p, cudaStream_t stream)
     }
     if constexpr (FORM != kScalar) {
         if (p.units <= 32)
-            return launch_overlapped(rope_append_kernel<FORM>, row_ctas, stream, p, split);
+            return launch_overlapped(row_ctas <= 2 * kSms ? rope_append_kernel<FORM, true>
+                                                     : rope_append_kernel<FORM, false>,
+                                     row_ctas, stream, p, split);
     }
     const int per = (p.Hq + 2 * p.Hkv) * p.units, pitch = (p.r / 2 + 7) / 8 * 8;
-    const int64_t many = std::min<int64_t>(std::min(kThreads / per, kMaxPairs / pitch), p.n / 608);
+    const int64_t many = std::min<int64_t>(std::min(kThreads / per, kMaxPairs / pitch), p.n / (4 * kSms));
     const int any_rows = many > 1 ? int(many) : 1;
     return launch_overlapped(rope_append_any_kernel<FORM>, (p.n + any_rows - 1) / any_rows, stream, p,
                              any_rows);
