@@ -414,16 +414,21 @@ __device__ __noinline__ void rescale_block(uint8_t *codes, int64_t row_bytes, in
     }
 }
 
+// The smallest byte with amax <= 448 * 2^(byte - 127), 448 = 1.75 * 2^8, but at least `old`.
+__device__ __forceinline__ int scale_code(float amax, int old)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    int code = int(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    code = code < 1 ? 1 : code;
+    return old > code ? old : code;
+}
+
 // The scale byte of a block and head (`old`, 0: started here) once rows of largest finite
 // magnitude amax join it: written where it changed, the codes so far rounded to it.
 __device__ __forceinline__ int settle(float amax, int old, uint8_t *codes, uint8_t *scale,
                                       int64_t row_bytes, int vecs, int lane)
 {
-    // the smallest byte with amax <= 448 * 2^(byte - 127): 448 = 1.75 * 2^8
-    const uint32_t bits = __float_as_uint(amax);
-    int code = int(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    code = code < 1 ? 1 : code;
-    code = old > code ? old : code;
+    const int code = scale_code(amax, old);
     __syncwarp();  // every lane has read the old byte
     if (lane == 0 && code != old)
         *scale = uint8_t(code);
@@ -586,19 +591,113 @@ __device__ __forceinline__ void append_run_128(const RopeParams &p, const Raw (&
     }
 }
 
+// Runs of one row (a decode step's), heads of 128 dims in vector form: eight lanes have a
+// head, a warp four heads of one row, a CTA eight heads of four rows at a time. Lane l has
+// the block, slot and position of row `first` + l; `singles` the lanes whose row is a run.
+// No barrier and no shared memory, unlike longer runs.
+template <int FORM>
+__device__ __forceinline__ void append_singles(const RopeParams &p, unsigned singles, int64_t first,
+                                               int64_t mine, int64_t slot, int64_t pos, bool is_v,
+                                               int h0, int warp, int lane)
+{
+    const int u = lane & 7, sub = lane >> 3;
+    const int64_t row_bytes = int64_t(p.Hkv) * 128;
+    const int h = h0 + (warp & 1) * 4 + sub;
+    const bool ok = h < p.Hkv;
+    int d0, d1;
+    unit_dims<FORM>(u, p.r, 128, d0, d1);
+    const int pairs = is_v ? 0 : FORM == kHalf ? (u < p.r / 16 ? 8 : 0)
+                                               : min(max(p.r / 2 - 8 * u, 0), 8);
+    for (int k = 0; singles != 0; ++k, singles &= singles - 1) {
+        if ((k & 3) != warp >> 1)
+            continue;
+        const int l0 = __ffs(singles) - 1;
+        const int64_t i = first + l0;
+        const int64_t block = __shfl_sync(kAll, mine, l0);
+        const int at = int(__shfl_sync(kAll, slot, l0)) & (kBlockSize - 1);
+        const int64_t position = __shfl_sync(kAll, pos, l0);
+        uint8_t *scale = (is_v ? p.v_scale : p.k_scale) + block * p.Hkv + h;
+        int old = 0;
+        Raw raw;
+        raw.a = raw.b = make_uint4(0, 0, 0, 0);
+        if (ok) {
+            if (at != 0)
+                old = *scale;
+            raw = load_raw((is_v ? p.v + i * p.v_stride : p.k + i * p.k_stride) + h * 128, d0, d1,
+                           128);
+        }
+        float2 t[8];
+        if (!is_v) {
+            // four lanes have the same unit of four heads: each computes two pairs for all
+            const float2 lo = sub < pairs ? turn(position, __ldg(p.turns + 8 * u + sub), p.scale)
+                                          : make_float2(0.f, 0.f);
+            const float2 hi = sub + 4 < pairs
+                                  ? turn(position, __ldg(p.turns + 8 * u + sub + 4), p.scale)
+                                  : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float2 from = c < 4 ? lo : hi;
+                t[c].x = __shfl_sync(kAll, from.x, (c & 3) * 8 + u);
+                t[c].y = __shfl_sync(kAll, from.y, (c & 3) * 8 + u);
+            }
+        }
+        float x[16];
+        unpack16(raw, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int m = FORM == kHalf ? c : 2 * c, n = FORM == kHalf ? c + 8 : 2 * c + 1;
+            if (c < pairs) {
+                const float v = x[m], w = x[n];
+                x[m] = v * t[c].x - w * t[c].y;
+                x[n] = w * t[c].x + v * t[c].y;
+            }
+        }
+        float amax = 0.f;  // of the finite ones
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            amax = fmaxf(amax, fabsf(x[c]) <= FLT_MAX ? fabsf(x[c]) : 0.f);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        const int code = scale_code(amax, old);
+        uint8_t *codes = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) +
+                         block * kBlockSize * row_bytes + h * 128;
+        __syncwarp();  // every lane has read the old byte
+        if (ok && u == 0 && code != old)
+            *scale = uint8_t(code);
+        // heads whose scale grew: the whole warp rounds their codes so far to it
+        for (unsigned grew = __ballot_sync(kAll, ok && u == 0 && old > 0 && code > old); grew != 0;
+             grew &= grew - 1) {
+            const int from = __ffs(grew) - 1;
+            const int64_t to = __shfl_sync(kAll, int64_t(reinterpret_cast<uintptr_t>(codes)),
+                                           from);
+            rescale_block(reinterpret_cast<uint8_t *>(to), row_bytes, 16,
+                          two_to(__shfl_sync(kAll, old - code, from)), lane);
+        }
+        __syncwarp();  // the new rows come after
+        if (ok) {
+            const float inv = two_to(127 - code);
+            uint8_t *row = codes + at * row_bytes;
+            *reinterpret_cast<uint2 *>(row + d0) = encode8(x, inv);
+            *reinterpret_cast<uint2 *>(row + d1) = encode8(x + 8, inv);
+        }
+    }
+}
+
 // Block-scaled E4M3 pools. `q_ctas` CTAs rotate q. Of the others, CTA (w, y) serves the
 // runs that start in the `window` rows from w * window on (a row starts one where the
 // row before it falls into another block), for eight heads of K (y even) or V, a warp
-// each: windows of one row while the rows are few (every token of a decode step is a
-// run of its own), of up to sixteen above (a prompt has a run in 16 rows, and a CTA
-// that finds none still costs its slot on an SM: 8,190 rows, K and V alone, 42.3 us with
-// eight rows looked at one after another, 24.9 us with one look at eight, 18.8 us at sixteen). Bound
-// by the latency of slots, then rows, then stores while rows are few (64 rows with q:
-// 3.9 us); at 8,190 rows of 64 q and 8 kv heads 53.3 us, 88% of the measured copy bandwidth.
+// each. A prompt has a run in 16 rows, and a CTA that finds none still costs its slot on an
+// SM: 8,190 rows, K and V alone, 42.3 us with eight rows looked at one after another, 24.9 us
+// with one look at eight, 18.8 us at sixteen. SINGLES: runs of one row apart, many at a time
+// (256 rows of a decode step, 32 q and 8 kv heads, 8.7 -> 4.4 us, 1000 rows 18.9 -> 7.7); not
+// for prompts, where the code beside it costs 8,190 rows 53.0 -> 55.1 us. Bound by the latency
+// of slots, then rows, then stores while rows are few (64 rows with q 3.3 us); at 8,190 rows
+// of 64 q and 8 kv heads 53.0 us, 88% of the measured copy bandwidth.
 // PASSES 0: heads of 128 dims in vector form.
-template <int FORM, int PASSES>
-__global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8_kernel(const RopeParams p, int split,
-                                                                   int64_t q_ctas, int window)
+template <int FORM, int PASSES, bool SINGLES = false>
+__global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2)
+    rope_append_fp8_kernel(const RopeParams p, int split, int64_t q_ctas, int window)
 {
     begin_after_previous();
     __shared__ float2 trig[kBlockSize * (kMaxFp8BlockDim / 2 + 8)];
@@ -638,8 +737,13 @@ __global__ void __launch_bounds__(kThreads, PASSES == 8 ? 1 : 2) rope_append_fp8
     const int64_t pos = in && !is_v ? __ldg(p.positions + first + lane) : 0;
     const int64_t mine = slot < 0 || slot >= p.total_slots ? -1 : slot / kBlockSize;
     const int64_t before = __shfl_up_sync(kAll, mine, 1);
-    const unsigned opens = __ballot_sync(kAll, lane >= 1 && lane <= window && mine >= 0 &&
-                                                          mine != before);
+    unsigned opens = __ballot_sync(kAll, lane >= 1 && lane <= window && mine >= 0 && mine != before);
+    if constexpr (SINGLES) {
+        const int64_t after = __shfl_down_sync(kAll, mine, 1);
+        const unsigned singles = opens & __ballot_sync(kAll, mine != after);
+        append_singles<FORM>(p, singles, first, mine, slot, pos, is_v, (y >> 1) * 8, warp, lane);
+        opens &= ~singles;
+    }
     for (unsigned left = opens; left != 0; left &= left - 1) {
         const int l0 = __ffs(left) - 1;  // the run's first row is lane l0's
         const int64_t i0 = first + l0;
@@ -719,27 +823,32 @@ template <int FORM>
 cudaError_t launch(const RopeParams &p, cudaStream_t stream)
 {
     constexpr int kWarps = kThreads / 32;
-    // Warps of a row: as many as leave two CTAs an SM (304) or fewer, and two at least. 600 rows
-    // of 32 q and 8 kv heads, 8 / 4 / 2 warps: 5.4 / 3.6 / 3.7 us; 1000: 7.4 / - / 4.8; 8,190,
-    // 1 / 2 / 4 warps: 34.9 / 33.8 / 36.9 (33.4 now, 88% of the measured copy bandwidth). Beside
-    // the block-scaled append, whose own arithmetic fills the issue slots, one once rows are
-    // many (each warp of a row computes its sines and cosines again): 8,190 rows, 1 / 2 / 4
-    // warps: 65.7 / 69.6 / 78.5 us (an earlier form of it).
-    const int wide = p.n <= 2 * kSms ? kWarps : p.n <= 4 * kSms ? 4 : 2;
-    const int split = p.k_scale && p.n >= 1024 ? 1 : wide;
+    // Warps of a row: as many as leave two CTAs an SM or fewer, and two at least (each warp of
+    // a row computes its sines and cosines again). 600 rows of 32 q and 8 kv heads, 8 / 4 / 2
+    // warps: 5.4 / 3.6 / 3.7 us; 1000: 7.4 / - / 4.8; 8,190, 1 / 2 / 4 warps: 34.9 / 33.8 / 36.9
+    // (33.4 now, 88% of the measured copy bandwidth).
+    int split = p.n <= 2 * kSms ? kWarps : p.n <= 4 * kSms ? 4 : 2, window = 0;
+    if (p.k_scale) {
+        // With the windows' CTAs beside them (eight kv heads or fewer); one warp once rows are
+        // many, for the append's own arithmetic fills the issue slots (8,190 rows, 1 / 2 / 4
+        // warps: 65.7 / 69.6 / 78.5 us, an earlier form). Windows of 2 / 4 / 8 at 8 or 4 warps,
+        // 400 rows of 32 q and 8 kv heads: 6.2 / - / 4.6 us where each is a run, 6.7 / - / 6.1
+        // in runs of four, 7.9 / - / 6.6 in one sequence; 128: 3.5 / 3.5 / 4.3, 4.1 / 4.0 / 5.8,
+        // 6.0 / 6.0 / 6.0.
+        const int64_t full = 2 * kSms;
+        window = p.n <= full * 2 / 3 ? 4 : p.n < 4096 ? 8 : 16;
+        split = p.n <= full * 2 / 3 ? kWarps : p.n <= full * 4 / 3 ? 4 : p.n <= full * 2 ? 2 : 1;
+    }
     const int rows = kWarps / split;
     const int64_t row_ctas = (p.n + rows - 1) / rows;
     if (p.k_scale) {
         const int64_t q_ctas = p.Hq == 0 ? 0 : FORM == kScalar ? p.n : row_ctas;
-        // (600 rows of 32 q and 8 kv heads, windows of 1 / 2 / 4 / 8: 14.2 / 13.3 / 14.6 / 18.3 us
-        // where each is a run, 10.1 / 8.4 / 6.9 / 8.1 in runs of four, 11.2 / 9.4 / 8.5 / 8.4 in
-        // one sequence; 128 rows, 1 / 2 / 4: 5.8 / 5.6 / 8.9, 4.5 / 4.0 / 3.9, 6.1 / 5.7 / 5.7)
-        const int window = p.n < 128 ? 1 : p.n < 512 ? 2 : p.n < 1024 ? 4 : p.n < 4096 ? 8 : 16;
         const int64_t grid = q_ctas + (p.n + window - 1) / window * 2 * ((p.Hkv + 7) / 8);
         if constexpr (FORM != kScalar) {
             if (p.D == 128)
-                return launch_overlapped(rope_append_fp8_kernel<FORM, 0>, grid, stream, p, split,
-                                         q_ctas, window);
+                return launch_overlapped(p.n < 4096 ? rope_append_fp8_kernel<FORM, 0, true>
+                                                    : rope_append_fp8_kernel<FORM, 0>,
+                                         grid, stream, p, split, q_ctas, window);
         }
         if (p.units * kBlockSize <= 32 * 4)
             return launch_overlapped(rope_append_fp8_kernel<FORM, 4>, grid, stream, p, split,

@@ -125,6 +125,29 @@ def test_large_batches_of_short_runs(n, new):
                 pkv.rotary_turns(128).numpy(), slots, rows(rng, slots.size, 2, 128))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n,Hq,Hkv,r", [(70, 8, 8, 128), (300, 5, 5, 64), (500, 9, 9, 48),
+                                        (1000, 2, 1, 128), (250, 0, 3, 24)])
+def test_decode_batches(n, Hq, Hkv, r, interleaved):
+    """One token of each sequence, three steps: blocks begun and continued, scales that grow
+    in some heads only, padding rows, and an infinity among the values."""
+    rng = np.random.default_rng(n + r)
+    pool = Pools(n + 2, Hkv, 128, seed=n, empty=False)
+    turns = pkv.rotary_turns(r).numpy()
+    block = rng.permutation(n + 2)[:n]
+    at = rng.integers(0, 14, n)
+    at[::5] = 0
+    for step in range(3):
+        slots = block * 16 + at + step
+        slots[rng.integers(0, n, n // 20 + 1)] = -1
+        size = 2.0 ** rng.integers(-4, 5, (n, Hkv, 1))
+        k = R.bf16(rng.standard_normal((n, Hkv, 128)) * size)
+        v = R.bf16(rng.standard_normal((n, Hkv, 128)) * size)
+        v[n // 2, 0, 5] = 0x7F80
+        pool.append(k, v, at + step + 1000 * np.arange(n), turns, slots,
+                    rows(rng, n, Hq, 128) if Hq else None, interleaved)
+
+
 def test_several_runs_and_padding():
     """Draft tokens of four sequences with padding behind each, one crossing a block."""
     rng = np.random.default_rng(8)
