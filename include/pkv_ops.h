@@ -150,6 +150,9 @@ pkv_status pkv_rope_kv_append_fp8_block(
  *                     3 scale / softcap is beyond float)
  *   alibi_slopes      device, float [num_q_heads], finite, or NULL
  *   window            >= 0; 0: no window (PKV_ERR_RANGE otherwise)
+ *   max_blocks_per_seq  how long a sequence may be: tables no wider than the batch
+ *                     needs let few or short sequences be finished in one launch
+ *                     (the results' rounding may differ with the width)
  *   workspace         >= pkv_workspace_size_scored(...) bytes, used as
  *                     pkv_paged_decode_attention uses its own
  * Other arguments, limits, errors and the error word as

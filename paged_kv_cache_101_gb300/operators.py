@@ -290,7 +290,8 @@ def _attend(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, n
 
 def paged_decode_attention_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables,
                                      context_lens, n_query_per_seq, scale, out, ws=None):
-    """Decode attention over block-scaled E4M3 (uint8) pools; writes ``out`` (bf16 or fp32)."""
+    """Decode attention over block-scaled E4M3 (uint8) pools; writes ``out`` (bf16 or fp32).
+    Tables no wider than the batch needs are faster where sequences are few or short."""
     if k_scale is None or v_scale is None:
         raise ValueError("k_scale and v_scale are required")
     return _attend(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
